@@ -338,6 +338,95 @@ RDT_API rdt_status rdt_head_rows(const rdt_config* cfg, const float* x, long lon
 RDT_API rdt_status rdt_greedy_tokens(const float* logits, int n, int vocab, int32_t* tokens, int out_ld,
                                      void* stream);
 
+/* ---- paged key / value cache --------------------------------------------------------------
+ * The K/V cache of rdt_kv_cache ("OpenMythos 분석", RoPE & generation cache: one cache per
+ * layer and recurrent loop) held in pages instead of one t_max stretch per sequence, so that
+ * memory is taken by the positions in use and sequences may share the pages of a common
+ * prefix.  The pages of the sources have no counterpart: the contents are those of
+ * rdt_kv_cache.  GQA only.  All pointers are caller-owned device memory.
+ *  Position t of sequence b lives in slot t % page_size of page
+ *  page_table[b * max_pages + t / page_size]; all loops use the same table.
+ *  kv_type 0: k, v [n_loops][n_pages][n_kv_heads][page_size][head_dim] in the model dtype.
+ *  kv_type 1: the same shape in e4m3 (1 byte), and k_exp, v_exp
+ *      [n_loops][n_pages][n_kv_heads][page_size] bytes: a stored row of head_dim values is
+ *      q * 2^(exp - 127), exp the smallest that brings the row's largest finite magnitude to at
+ *      most 448 (0 for a row of zeros), q rounded to nearest even.  Infinities are stored as NaN.
+ * Table entries of positions past a sequence's length are never read.  An entry out of range
+ * that is needed is recorded as RDT_ERR_DEVICE_BOUNDS and its positions are left out. */
+typedef struct {
+  void* k;
+  void* v;
+  uint8_t* k_exp;             /* kv_type 1, else NULL                                    */
+  uint8_t* v_exp;
+  const int32_t* page_table;  /* [batch][max_pages] device                               */
+  int dtype;                  /* model dtype: 0 = fp32, 1 = bf16                         */
+  int kv_type;                /* 0 = model dtype, 1 = e4m3 with exponent bytes           */
+  int n_loops, n_pages, page_size;
+  int n_kv_heads, head_dim;   /* head_dim <= 256                                         */
+  int batch, max_pages;       /* table rows, entries of one row                          */
+} rdt_paged_cache;
+
+/* Write n_rows rows of keys and values (model dtype; row i, kv head g at i * row_ld +
+ * g * head_dim elements of k and v) into loop `loop` of the cache, quantising as they are
+ * written when kv_type is 1.  Row i belongs to sequence i / seq (n_rows a multiple of seq, at
+ * most batch * seq) and sits at position positions[i] (device int32); a negative position is a
+ * padding row, of which nothing is written.  Two rows of one call must not name one slot.
+ * status: NULL, or a 16-byte device status word (zeroed by the caller before its first use;
+ * rdt_read_device_status reads and clears it). */
+RDT_API rdt_status rdt_paged_kv_write(const rdt_paged_cache* cache, int loop, const void* k, const void* v,
+                                      long long row_ld, const int32_t* positions, int n_rows, int seq,
+                                      void* status, void* stream);
+
+/* Read positions 0 .. min(lens[b], t_out) - 1 of sequences 0 .. batch - 1 back from loop `loop`:
+ * k_out, v_out [batch][n_kv_heads][t_out][head_dim] in the model dtype (the layout of a loop of
+ * rdt_kv_cache).  Later positions of the outputs are left as they were.  lens: device int32. */
+RDT_API rdt_status rdt_paged_kv_read(const rdt_paged_cache* cache, int loop, const int32_t* lens, int batch,
+                                     int t_out, void* k_out, void* v_out, void* status, void* stream);
+
+/* One-token attention over the cache: for query head h of sequence b, kv head
+ * h / (n_heads / n_kv_heads), o = sum_j softmax_j(q . k_j * scale) v_j over the positions
+ * j < lens[b] (device int32; the new token's own position is written before the call).  A
+ * sequence with lens[b] <= 0 gives zeros.  q, o: [batch][n_heads][head_dim] model dtype with
+ * q_ld / o_ld elements between sequences (>= n_heads * head_dim); o must not overlap q or the
+ * cache.  ws: rdt_paged_attention_workspace_size bytes, 256-byte aligned, used by one call at
+ * a time (calls on one stream in order may share it); its contents need no initialisation. */
+RDT_API size_t rdt_paged_attention_workspace_size(const rdt_paged_cache* cache, int batch, int n_heads);
+RDT_API rdt_status rdt_paged_attention(const rdt_paged_cache* cache, int loop, const void* q, long long q_ld,
+                                       const int32_t* lens, int batch, int n_heads, float scale, void* o,
+                                       long long o_ld, void* ws, size_t ws_bytes, void* status, void* stream);
+
+/* ---- sampled next token -------------------------------------------------------------------
+ * The generation loop is printed without a sampling rule; rdt_greedy_tokens is its plainest
+ * reading, and this is the usual one.  Per row of logits x with maximum m and temperature T,
+ * token v weighs w_v = exp((x_v - m) / T), rounded to multiples of 2^-44.  In the order of the logits,
+ * ties by the lower index: top_k > 0 keeps the first top_k tokens; top_p < 1 keeps, of these,
+ * the tokens whose preceding tokens hold less than top_p of their weight; min_p > 0 keeps, of
+ * these, those with w_v >= min_p.  The first token of the order always stays.  The result is
+ * the first v, by index, at which the running sum of the kept weights exceeds u * their total.
+ * NaN logits take no part.  T <= 0, and rows of nothing but -inf and NaN: the token of
+ * rdt_greedy_tokens.  The scalars are checked (T >= 0 and finite, top_k >= 0, 0 < top_p <= 1,
+ * 0 <= min_p <= 1); a per-row device array [n] that is not NULL takes the scalar's place, and
+ * there T NaN or <= 0 means greedy, top_k <= 0 and top_p NaN or >= 1 mean off, top_p <= 0
+ * keeps one token, min_p NaN or <= 0 means off and min_p > 1 is 1. */
+typedef struct {
+  float temperature;
+  int top_k;
+  float top_p;
+  float min_p;
+  const float* temperature_rows;
+  const int32_t* top_k_rows;
+  const float* top_p_rows;
+  const float* min_p_rows;
+} rdt_sampling;
+
+/* logits [n] rows of vocab fp32, ld floats apart (ld >= vocab, vocab < 2^20); u [n] fp32
+ * uniform numbers in [0, 1) (others are clamped, NaN is 0); tokens[b * out_ld] int32; logprob:
+ * NULL or [n] fp32, the natural logarithm of the drawn token's probability among the kept ones
+ * (0 for a greedy row).  The same inputs give the same tokens on every call. */
+RDT_API rdt_status rdt_sample_tokens(const float* logits, long long ld, int n, int vocab, const float* u,
+                                     const rdt_sampling* params, int32_t* tokens, int out_ld, float* logprob,
+                                     void* stream);
+
 /* out[i] = x[i] in the model dtype (fp32 copy, or bf16 round-to-nearest-even), i < n:
  * the recurrent block's injected input e is the prelude output in the model dtype
  * ("OpenMythos 분석", Core Structure: e = x after the prelude).  Device pointers. */

@@ -9,3 +9,5 @@ from .api import (RecurrentBlock, KVCache, Trace, Block, Generator, DecodeGraph,
                   embed, head,
                   model_forward, generate, greedy_tokens, to_model_dtype, config_struct, dense_config_struct,
                   workspace_size, alloc_workspace)
+from .serving import (PagedKVCache, paged_kv_write, paged_kv_read, paged_attention,  # noqa: F401
+                      paged_attention_workspace, sample_tokens)

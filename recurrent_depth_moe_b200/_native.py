@@ -59,6 +59,19 @@ class rdt_depth_batch(ctypes.Structure):
                 ("expert_ids", c_void_p), ("cache", POINTER(rdt_kv_cache)), ("ws", c_void_p), ("ws_bytes", c_size_t)]
 
 
+class rdt_paged_cache(ctypes.Structure):
+    _fields_ = [("k", c_void_p), ("v", c_void_p), ("k_exp", c_void_p), ("v_exp", c_void_p),
+                ("page_table", c_void_p)] + [(n, c_int) for n in (
+                    "dtype", "kv_type", "n_loops", "n_pages", "page_size", "n_kv_heads", "head_dim", "batch",
+                    "max_pages")]
+
+
+class rdt_sampling(ctypes.Structure):
+    _fields_ = [("temperature", c_float), ("top_k", c_int), ("top_p", c_float), ("min_p", c_float),
+                ("temperature_rows", c_void_p), ("top_k_rows", c_void_p), ("top_p_rows", c_void_p),
+                ("min_p_rows", c_void_p)]
+
+
 class rdt_kernel_time(ctypes.Structure):
     _fields_ = [("name", ctypes.c_char * 32), ("launches", c_int), ("total_ms", ctypes.c_double)]
 
@@ -69,7 +82,9 @@ EXPORTS = ("rdt_workspace_size", "rdt_recurrent_forward", "rdt_recurrent_decode_
            "rdt_launch_count", "rdt_profile_start", "rdt_profile_stop", "rdt_recurrent_decode_step_static",
            "rdt_read_static_status", "rdt_recurrent_decode_step_ex",
            "rdt_depth_batch_workspace_size", "rdt_depth_batch_begin", "rdt_depth_batch_tick",
-           "rdt_depth_batch_pending", "rdt_depth_batch_run")
+           "rdt_depth_batch_pending", "rdt_depth_batch_run",
+           "rdt_paged_kv_write", "rdt_paged_kv_read", "rdt_paged_attention_workspace_size", "rdt_paged_attention",
+           "rdt_sample_tokens")
 
 _lib = None
 _profiling = False
@@ -124,6 +139,16 @@ def load(path: str = LIB_PATH):
     lib.rdt_embed.restype = c_int
     lib.rdt_head.argtypes = [POINTER(rdt_config), P, c_int, P, P, c_int, P, P, c_size_t, P]
     lib.rdt_head.restype = c_int
+    C = POINTER(rdt_paged_cache)
+    lib.rdt_paged_kv_write.argtypes = [C, c_int, P, P, ctypes.c_longlong, P, c_int, c_int, P, P]
+    lib.rdt_paged_kv_read.argtypes = [C, c_int, P, c_int, c_int, P, P, P, P]
+    lib.rdt_paged_attention_workspace_size.argtypes = [C, c_int, c_int]
+    lib.rdt_paged_attention_workspace_size.restype = c_size_t
+    lib.rdt_paged_attention.argtypes = [C, c_int, P, ctypes.c_longlong, P, c_int, c_int, c_float, P,
+                                        ctypes.c_longlong, P, c_size_t, P, P]
+    lib.rdt_sample_tokens.argtypes = [P, ctypes.c_longlong, c_int, c_int, P, POINTER(rdt_sampling), P, c_int, P, P]
+    for fn in ("rdt_paged_kv_write", "rdt_paged_kv_read", "rdt_paged_attention", "rdt_sample_tokens"):
+        getattr(lib, fn).restype = c_int
     lib.rdt_read_device_status.argtypes = [P, P]
     lib.rdt_read_device_status.restype = c_int
     lib.rdt_status_string.argtypes = [c_int]

@@ -249,4 +249,55 @@ void launch_embed(int dtype, const void* table, int vocab, const int* ids, int n
 void launch_trace_rows(int src_is_model_dtype, int dtype, const void* src, int W, int row0, int n,
                        const float* bias, float* dst, cudaStream_t s);
 
+// ------------------------------------------------------------------------------------------
+// paged key / value cache: pages [n_pages][Hkv][page_size][hd] of one loop, sequence b's
+// position t in slot t % page_size of page table[b * max_pages + t / page_size]
+// ------------------------------------------------------------------------------------------
+struct PagedView {
+  void* k; void* v;              // this loop's pages, model dtype or e4m3
+  uint8_t* ke; uint8_t* ve;      // e4m3: exponent bytes [n_pages][Hkv][page_size]
+  const int* table;
+  int e4m3, n_pages, page_size, Hkv, hd, max_pages;
+};
+struct PagedWriteParams {
+  PagedView c;
+  const void* k; const void* v; long long ld;   // row i, kv head g at i * ld + g * hd
+  const int* pos;                               // [n_rows] position, < 0: nothing written
+  int n_rows, seq;                              // row i belongs to sequence i / seq
+  DevStatus* st;
+};
+struct PagedReadParams {
+  PagedView c;
+  const int* lens; int len_add;                 // positions 0 .. lens[b] + len_add - 1
+  int B, t_out;
+  void* k_out; void* v_out;                     // [B][Hkv][t_out][hd] model dtype
+  DevStatus* st;
+};
+struct PagedAttnParams {
+  PagedView c;
+  const void* q; long long q_row;               // [B][H][hd], row b at b * q_row
+  void* o; long long o_row;
+  const int* lens; int len_add;                 // visible keys of sequence b: lens[b] + len_add
+  int B, H;
+  float scale;
+  void* scratch;                                // paged_attn_scratch() bytes
+  float* part_o; float* part_ml;
+  DevStatus* st;
+};
+void launch_paged_write(int dtype, const PagedWriteParams& p, cudaStream_t s);
+void launch_paged_read(int dtype, const PagedReadParams& p, cudaStream_t s);
+size_t paged_attn_scratch(int dtype, const PagedView& c, int B, int H);
+int launch_paged_attn(int dtype, const PagedAttnParams& p, cudaStream_t s);   // returns 0 on success
+
+struct SampleParams {
+  const float* logits; long long ld;
+  int n, vocab;
+  const float* u;                               // [n] uniform numbers in [0, 1)
+  float temperature; int top_k; float top_p, min_p;
+  const float* temperature_row; const int* top_k_row; const float* top_p_row; const float* min_p_row;   // [n] or null
+  int* tokens; int out_ld;
+  float* logprob;                               // [n] or null
+};
+void launch_sample(const SampleParams& p, cudaStream_t s);
+
 }  // namespace rdt
