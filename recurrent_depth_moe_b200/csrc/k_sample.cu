@@ -9,223 +9,622 @@
 // order, at which the running sum of the kept weights exceeds u times their total.
 // NaN logits take no part.  T <= 0, or a row with no weight: the most likely token.
 //
-// Weights are rounded to whole numbers of 2^-44, so every sum is exact
-// whatever its order, the same on every run, and a border cannot be missed between two passes.
-// The exponent (x - m) log2(e) / T is formed in two fp32 words, so a weight is off by about
-// one rounding of its 24 bits wherever it lies.
+// Weights are rounded to whole numbers of 2^-44, so every sum is exact whatever its order, the
+// same on every run, and a border cannot be missed between two passes.  The exponent
+// (x - m) log2(e) / T is formed in two fp32 words, so a weight is off by about one rounding of
+// its 24 bits wherever it lies.
+//
+// A cluster of up to 8 CTAs holds one row in its shared memory, so the logits are read from
+// HBM once; sums, histograms and candidates travel through distributed shared memory and no
+// workspace is needed.  Without the row on chip each of the up to four passes would read it
+// again.  The order is never sorted: a histogram over the exponent (1/16 of a power of two per
+// bin) brackets the border of top-k or top-p, the few tokens of the bracket become candidates,
+// and histograms over their (logit, index) order narrow the border to at most 32 of them, which
+// one warp ranks.  The kept tokens are then those at or before one (logit, index) pair.
 #include "common.cuh"
 #include "kernels.h"
+
+#include <cooperative_groups.h>
+
+#include <algorithm>
+
+namespace cg = cooperative_groups;
 
 namespace rdt {
 
 namespace {
-constexpr int NT = 1024, NW = NT / 32;
+constexpr int NT = 512, NW = NT / 32;
+constexpr int BINS = 46 * 16;    // of the exponent: below 2^-46 a weight rounds to nothing
+constexpr int RB = 256;          // bins of one refinement
+constexpr int LCAP = 1024;       // candidates one CTA lists; more are found by passes over the row
+constexpr int IDX_BITS = 20;
 typedef unsigned long long u64;
 
-// order of floats as unsigned integers; NaN below everything
+// order of floats as unsigned integers
 __device__ __forceinline__ uint32_t key_of(float x) {
   const uint32_t b = __float_as_uint(x + 0.f);   // -0 and 0 are the same logit
-  if (x != x) return 0u;
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 __device__ __forceinline__ float of_key(uint32_t k) { return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k); }
+// place in the order: larger comes first, and no two tokens share one
+__device__ __forceinline__ u64 place_of(float x, int v) {
+  return ((u64)key_of(x) << IDX_BITS) | (uint32_t)((1 << IDX_BITS) - 1 - v);
+}
 
+// z = x log2(e) / T as zh + e, in two fp32 words; the weight is 2^(z - M), M that of the maximum.
 struct Weigh {
-  float m, chi, clo;   // maximum; log2(e) / T in two words
+  float m, chi, clo, nfM, c16;   // log2(e) / T in two words; minus M's fraction; bins per logit
+  int i0;                        // M's whole part (as the bits of i + MAGIC)
+  bool wide;                     // |M| so large that z has no fraction left: the difference m - x is formed first
+  static constexpr float MAGIC = 12582912.f;   // 1.5 * 2^23: x + MAGIC rounds x to a whole number
   __device__ Weigh(float mx, float T) : m(mx) {
     const double c = 1.4426950408889634074 / (double)T;
     chi = (float)c;
     clo = isinf(chi) ? 0.f : (float)(c - (double)chi);
+    c16 = fminf(16.f * chi, 3.0e38f);
+    const float Mh = mx * chi;
+    wide = !(fabsf(Mh) <= 65536.f);
+    const float r = Mh + MAGIC;
+    i0 = __float_as_int(r);
+    nfM = -((Mh - (r - MAGIC)) + (fmaf(mx, chi, -Mh) + mx * clo));
   }
-  // weight of x in units of 2^-44
+  // 16 times the exponent, monotone in x; NaN for NaN
+  __device__ __forceinline__ float t16(float x) const { return (m - x) * c16; }
+  // the weight in units of 2^-44 is q << sh; 0 <= t16(x) < BINS
+  __device__ __forceinline__ void parts(float x, uint32_t& q, int& sh) const {
+    float s;
+    int k;
+    if (!wide) {
+      const float zh = x * chi, r = zh + MAGIC;
+      s = ((zh - (r - MAGIC)) + fmaf(x, clo, nfM)) + fmaf(x, chi, -zh);
+      k = i0 - __float_as_int(r);
+    } else {
+      const float d = m - x, t = d * chi, bb = d - m;
+      const float dlo = (m - (d - bb)) + (-x - bb);                // d + dlo = m - x
+      const float r = t + MAGIC;
+      s = x == m ? 0.f : -((t - (r - MAGIC)) + (fmaf(d, chi, -t) + fmaf(d, clo, dlo * chi)));
+      k = x == m ? 0 : min(47, __float_as_int(r) - __float_as_int(MAGIC));   // 47: log2(e) / T overflows (q is 0)
+    }
+    const int kk = max(k, 20);
+    sh = kk - k;
+    q = __float2uint_rn(exp2f(s) * __int_as_float((171 - kk) << 23));   // 2^(44 - kk)
+  }
   __device__ __forceinline__ u64 operator()(float x) const {
-    if (x == m) return 1ull << 44;
-    const float d = m - x, t = d * chi;
-    if (!(t < 46.f)) return 0;                                   // also NaN and -inf
-    const float bb = d - m;
-    const float dlo = (m - (d - bb)) + (-x - bb);                // d + dlo = m - x
-    const float e = fmaf(d, chi, -t) + fmaf(d, clo, dlo * chi);  // t + e = (m - x) log2(e) / T
-    const int i = __float2int_rn(t);
-    const float w = exp2f(-((t - (float)i) + e));                // 2^-1/2 .. 2^1/2
-    return (((u64)(uint32_t)(w * 16777216.f) << 21 >> i) + 1) >> 1;
+    uint32_t q;
+    int sh;
+    parts(x, q, sh);
+    return (u64)q * (u64)(1u << sh);
   }
 };
 
-__device__ u64 block_sum64(u64 v, u64* red) {
+struct Shared {
+  u64 mass[2][RB];
+  u64 wsum[NW];          // kept weight of each warp's piece of the row
+  u64 glist[2][32];      // [top-k, top-p] the last candidates
+  u64 red[NW];
+  u64 bc[3];
+  u64 total, above;
+  uint32_t hist[BINS];
+  uint32_t cnt[2][RB];
+  uint32_t list[LCAP];
+  uint32_t fcnt[2], gcnt[2], kmin[2], kmax[2];
+  uint32_t idx;
+  int ib[4];
+  float fred[NW];
+  float mx;
+};
+
+template <typename V> __device__ __forceinline__ V warp_scan(V v) {   // inclusive
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  for (int o = 1; o < 32; o <<= 1) {
+    const V t = __shfl_up_sync(0xffffffffu, v, o);
+    if ((int)(threadIdx.x & 31) >= o) v += t;
+  }
+  return v;
+}
+// Inclusive sum over the block's threads; `red` holds NW values, `total` the block's.
+template <typename V> __device__ __forceinline__ V block_scan(V v, V* red, V& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  v = warp_scan(v);
   __syncthreads();
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  if (lane == 31) red[warp] = v;
   __syncthreads();
-  v = red[threadIdx.x & 31];
+  const V w = warp_scan(lane < NW ? red[lane] : (V)0);
+  total = __shfl_sync(0xffffffffu, w, NW - 1);
+  const V before = __shfl_sync(0xffffffffu, w, max(warp - 1, 0));
+  return warp ? v + before : v;
+}
+__device__ __forceinline__ u64 warp_sum64(u64 v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
 
-struct Cut {
-  uint32_t key;   // the last key that stays
-  u64 ties;       // of the tokens at that key, how many stay (from the lowest index)
-  u64 before;     // measure (count or weight) of the tokens above the key
+// RES: the CTA's piece of the row lives in shared memory; else (a row too long for the cluster)
+// every pass reads it again.
+template <bool RES> struct Row {
+  const float* row;
+  const float4* chunk;   // RES: the piece
+  int V, a, q0, nq;      // the row starts a floats past a 16-byte boundary; quads q0 .. q0 + nq - 1 are this CTA's
+  int jb, je;            // this warp's quads, contiguous
+  bool inf_row;          // the maximum is +inf: the infinities weigh 1, the rest nothing
+  __device__ __forceinline__ float4 load(int j) const {
+    const int i = 4 * (q0 + j) - a;
+    if (i >= 0 && i + 4 <= V) return __ldg(reinterpret_cast<const float4*>(row + i));
+    const float none = __int_as_float(0x7fffffff);   // past the row's ends: NaN, which takes no part
+    float4 v;
+    v.x = i >= 0 && i < V ? row[i] : none;
+    v.y = i + 1 >= 0 && i + 1 < V ? row[i + 1] : none;
+    v.z = i + 2 >= 0 && i + 2 < V ? row[i + 2] : none;
+    v.w = i + 3 >= 0 && i + 3 < V ? row[i + 3] : none;
+    return v;
+  }
+  __device__ __forceinline__ float fix(float x) const { return !inf_row ? x : x == INFINITY ? 0.f : -INFINITY; }
+  __device__ __forceinline__ float4 quad(int j) const {
+    if (RES) return chunk[j];
+    const float4 v = load(j);
+    return make_float4(fix(v.x), fix(v.y), fix(v.z), fix(v.w));
+  }
+  __device__ __forceinline__ int index(int local) const { return 4 * q0 + local - a; }
+  __device__ __forceinline__ float at(int local) const {
+    return RES ? reinterpret_cast<const float*>(chunk)[local] : fix(row[index(local)]);
+  }
+  // f(x, local index) for every element of the warp's piece, in no order across lanes
+  template <typename F> __device__ __forceinline__ void each(F f) const {
+#pragma unroll 2
+    for (int j = jb + (threadIdx.x & 31); j < je; j += 32) {
+      const float4 v = quad(j);
+      f(v.x, 4 * j); f(v.y, 4 * j + 1); f(v.z, 4 * j + 2); f(v.w, 4 * j + 3);
+    }
+  }
 };
 
-// The key at which the running measure of the order (count, or weight) reaches `want` >= 1:
-// four passes, 8 bits of the key each.
-template <bool MASS>
-__device__ Cut select(const float* row, int V, const Weigh& wt, u64 want, u64* hist, u64* sh) {
-  uint32_t prefix = 0;
-  u64 before = 0;
-  for (int level = 3; level >= 0; --level) {
-    const int sft = level * 8;
-    for (int i = threadIdx.x; i < 256; i += NT) hist[i] = 0;
-    __syncthreads();
-    for (int v = threadIdx.x; v < V; v += NT) {
-      const uint32_t k = key_of(row[v]);
-      if (level < 3 && (k >> (sft + 8)) != (prefix >> (sft + 8))) continue;
-      const u64 q = MASS ? wt(row[v]) : 1ull;
-      if (q) atomicAdd(&hist[(k >> sft) & 255], q);
-    }
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      u64 c = before;
-      int bin = 255;
-      for (; bin > 0; --bin) {
-        if (c + hist[bin] >= want) break;
-        c += hist[bin];
-      }
-      sh[0] = c;
-      sh[1] = (u64)bin;
-    }
-    __syncthreads();
-    before = sh[0];
-    prefix |= (uint32_t)sh[1] << sft;
-    __syncthreads();
+// Which tokens are in play: bin below L, or in bin L and at or before `place`.
+struct Cut {
+  float L;
+  u64 place;
+  __device__ __forceinline__ bool holds(float t, float x, int v) const {
+    return t < L || (t < L + 1.f && t < (float)BINS && place_of(x, v) >= place);
   }
-  Cut r;
-  r.key = prefix;
-  r.before = before;
-  const u64 unit = MASS ? wt(of_key(prefix)) : 1ull;
-  r.ties = unit ? (want - before + unit - 1) / unit : ~0ull;
-  return r;
-}
+};
+
+template <bool RES> struct Sampler {
+  cg::cluster_group cl;
+  Shared& sh;
+  const Row<RES>& row;
+  const Weigh& wt;
+  int C, level;
+  __device__ __forceinline__ Sampler(Shared& s, const Row<RES>& r, const Weigh& w)
+      : cl(cg::this_cluster()), sh(s), row(r), wt(w), C((int)cl.num_blocks()), level(0) {}
+
+  // Sum of the cluster's histograms, one pair of bins per thread.
+  __device__ __forceinline__ void pair_counts(u64& c0, u64& c1) {
+    c0 = c1 = 0;
+    const int b = 2 * threadIdx.x;
+    if (b < BINS)
+      for (int r = 0; r < C; ++r) {
+        const uint2 h = *reinterpret_cast<const uint2*>(cl.map_shared_rank(sh.hist, r) + b);
+        c0 += h.x;
+        c1 += h.y;
+      }
+  }
+  // Note an element as a candidate of phase ph.
+  __device__ __forceinline__ void candidate(int ph, float x, int local) {
+    const uint32_t n = atomicAdd(&sh.fcnt[ph], 1u), k = key_of(x);
+    if (n < LCAP) sh.list[n] = local;
+    atomicMin(&sh.kmin[ph], k);
+    atomicMax(&sh.kmax[ph], k);
+  }
+  // f(x, token) for the CTA's candidates of phase ph with places lo .. hi: its list, or
+  // (`all`) every element that `in` holds.
+  template <typename F> __device__ __forceinline__ void candidates(int ph, bool all, const Cut& in, u64 lo, u64 hi, F f) {
+    if (!all) {
+      for (uint32_t i = threadIdx.x; i < sh.fcnt[ph]; i += NT) {
+        const int l = sh.list[i], v = row.index(l);
+        const float x = row.at(l);
+        const u64 pl = place_of(x, v);
+        if (pl >= lo && pl <= hi) f(x, pl);
+      }
+    } else {
+      const float xlo = of_key((uint32_t)(lo >> IDX_BITS));
+      row.each([&](float x, int l) {
+        if (!(x >= xlo)) return;
+        const int v = row.index(l);
+        const u64 pl = place_of(x, v);
+        if (pl >= lo && pl <= hi && in.holds(wt.t16(x), x, v)) f(x, pl);
+      });
+    }
+  }
+  // The last place that stays: in the order of the candidates lo .. hi (n of them), with `base`
+  // of the measure (their number, or with MASS their weight) before them, the one at which the
+  // running measure reaches `want`.  False: it is not reached.  The candidates are narrowed by
+  // RB at a time.
+  template <bool MASS>
+  __device__ bool resolve(int ph, bool all, const Cut& in, u64 lo, u64 hi, u64 n, u64 base, u64 want, u64& place) {
+    bool first = true;
+    while (n > 32 || first) {
+      if (n <= 32 && !all) break;
+      first = false;
+      const int par = level++ & 1;   // the other half may still be read by the cluster
+      for (int i = threadIdx.x; i < RB; i += NT) sh.mass[par][i] = 0, sh.cnt[par][i] = 0;
+      __syncthreads();
+      const int s = max(0, 64 - __clzll((long long)(hi - lo)) - 8);
+      candidates(ph, all, in, lo, hi, [&](float x, u64 pl) {
+        const int b = (int)((hi - pl) >> s);
+        atomicAdd(&sh.cnt[par][b], 1u);
+        if (MASS) atomicAdd(&sh.mass[par][b], wt(x));
+      });
+      cl.sync();
+      u64 c = 0, m = 0;
+      if (threadIdx.x < RB)
+        for (int r = 0; r < C; ++r) {
+          c += cl.map_shared_rank(&sh.cnt[par][0], r)[threadIdx.x];
+          if (MASS) m += cl.map_shared_rank(&sh.mass[par][0], r)[threadIdx.x];
+        }
+      if (!MASS) m = c;
+      u64 total;
+      const u64 incl = block_scan(m, sh.red, total);
+      if (base + total < want) return false;
+      if (base + incl - m < want && want <= base + incl) {
+        sh.ib[0] = threadIdx.x;
+        sh.bc[0] = base + incl - m;
+        sh.bc[1] = c;
+      }
+      __syncthreads();
+      const u64 b = sh.ib[0];
+      base = sh.bc[0];
+      n = sh.bc[1];
+      hi -= b << s;
+      const u64 span = (1ull << s) - 1;
+      if (hi - lo > span) lo = hi - span;
+      __syncthreads();
+    }
+    candidates(ph, all, in, lo, hi, [&](float, u64 pl) {
+      const uint32_t i = atomicAdd(&sh.gcnt[ph], 1u);
+      if (i < 32) sh.glist[ph][i] = pl;
+    });
+    cl.sync();
+    if (threadIdx.x < 32) {
+      u64 pl = 0;
+      int at = threadIdx.x;
+      for (int r = 0; r < C; ++r) {
+        const int g = min(32, (int)*cl.map_shared_rank(&sh.gcnt[ph], r));
+        if (at >= 0 && at < g) pl = cl.map_shared_rank(&sh.glist[ph][0], r)[at];
+        at -= g;
+      }
+      u64 w = 0, before = base;
+      if (pl) w = MASS ? wt(of_key((uint32_t)(pl >> IDX_BITS))) : 1;
+#pragma unroll
+      for (int j = 0; j < 32; ++j) {
+        const u64 opl = __shfl_sync(0xffffffffu, pl, j), ow = __shfl_sync(0xffffffffu, w, j);
+        if (opl > pl) before += ow;
+      }
+      u64 mine = pl && before < want ? pl : ~0ull;
+      u64 reach = pl ? before + w : 0;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        mine = min(mine, __shfl_xor_sync(0xffffffffu, mine, o));
+        reach = max(reach, __shfl_xor_sync(0xffffffffu, reach, o));
+      }
+      if (threadIdx.x == 0) sh.bc[2] = reach >= want ? mine : 0;
+    }
+    __syncthreads();
+    place = sh.bc[2];
+    return place != 0;
+  }
+};
 }  // namespace
 
-__global__ void __launch_bounds__(NT) k_sample(SampleParams p) {
-  __shared__ u64 hist[256], red[NW], sh[2], wsum[NW];
-  __shared__ float fmx[NW];
-  __shared__ int found;
-  const int r = blockIdx.x, V = p.vocab, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const float* row = p.logits + (long long)r * p.ld;
+template <bool RES>
+__global__ void __launch_bounds__(NT, 2) k_sample(SampleParams p, int chunk_quads) {
+  extern __shared__ __align__(16) float4 chunk[];
+  __shared__ Shared sh;
+  cg::cluster_group cl = cg::this_cluster();
+  const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
+  const int r = blockIdx.x / C, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const float T = p.temperature_row ? p.temperature_row[r] : p.temperature;
   const int k = p.top_k_row ? p.top_k_row[r] : p.top_k;
   const float top_p = p.top_p_row ? p.top_p_row[r] : p.top_p;
   const float min_p = p.min_p_row ? p.min_p_row[r] : p.min_p;
+  Row<RES> row;
+  row.row = p.logits + (long long)r * p.ld;
+  row.chunk = chunk;
+  row.V = p.vocab;
+  row.a = (int)((reinterpret_cast<uintptr_t>(row.row) >> 2) & 3);
+  row.nq = max(0, min(chunk_quads, (p.vocab + row.a + 3) / 4 - rank * chunk_quads));
+  row.q0 = rank * chunk_quads;
+  const int piece = (chunk_quads + NW - 1) / NW;   // quads of a warp
+  row.jb = min(row.nq, warp * piece);
+  row.je = min(row.nq, row.jb + piece);
+  row.inf_row = false;
+  for (int i = tid; i < BINS; i += NT) sh.hist[i] = 0;
+  if (tid < 2) sh.fcnt[tid] = sh.gcnt[tid] = sh.kmax[tid] = 0, sh.kmin[tid] = ~0u;
+  if (tid == 0) sh.idx = 0x7fffffff;
   float mx = -INFINITY;
-  for (int v = tid; v < V; v += NT) mx = fmaxf(mx, row[v]);      // fmaxf drops NaN
+#pragma unroll 4
+  for (int j = row.jb + lane; j < row.je; j += 32) {
+    const float4 v = row.load(j);
+    if (RES) chunk[j] = v;
+    mx = fmaxf(fmaxf(mx, fmaxf(v.x, v.y)), fmaxf(v.z, v.w));   // fmaxf drops NaN
+  }
   mx = warp_max(mx);
-  if (lane == 0) fmx[warp] = mx;
+  if (lane == 0) sh.fred[warp] = mx;
   __syncthreads();
-  mx = warp_max(fmx[lane]);
-  if (tid == 0) found = 0x7fffffff;
-  __syncthreads();
+  if (warp == 0) {
+    mx = warp_max(lane < NW ? sh.fred[lane] : -INFINITY);
+    if (lane == 0) sh.mx = mx;
+  }
+  cl.sync();
+  mx = warp_max(lane < C ? *cl.map_shared_rank(&sh.mx, lane) : -INFINITY);
   if (!(T > 0.f) || mx == -INFINITY) {                           // the most likely token
-    int best = 0x7fffffff;
-    for (int v = tid; v < V && best == 0x7fffffff; v += NT)
-      if (row[v] == mx) best = v;
-    atomicMin(&found, best);
-    __syncthreads();
-    if (tid == 0) {
-      p.tokens[(long long)r * p.out_ld] = found == 0x7fffffff ? 0 : found;
+    uint32_t best = 0x7fffffff;
+    row.each([&](float x, int l) { if (x == mx) best = min(best, (uint32_t)row.index(l)); });
+    if (best != 0x7fffffff) atomicMin(&sh.idx, best);
+    cl.sync();
+    if (rank == 0 && tid == 0) {
+      for (int i = 0; i < C; ++i) best = min(best, *cl.map_shared_rank(&sh.idx, i));
+      p.tokens[(long long)r * p.out_ld] = best == 0x7fffffff ? 0 : (int)best;
       if (p.logprob) p.logprob[r] = 0.f;
     }
+    cl.sync();                                                   // remote shared memory is read until here
     return;
   }
+  if (mx == INFINITY) {
+    row.inf_row = true;
+    if (RES)
+      for (int j = row.jb + lane; j < row.je; j += 32) {
+        const float4 v = chunk[j];
+        chunk[j] = make_float4(row.fix(v.x), row.fix(v.y), row.fix(v.z), row.fix(v.w));
+      }
+    mx = 0.f;
+  }
   const Weigh wt(mx, T);
-  Cut cut{0u, ~0ull, 0};
-  if (k > 0 && k < V) cut = select<false>(row, V, wt, (u64)k, hist, sh);
-  if (top_p < 1.f) {
-    u64 above = 0, ties = 0;
-    for (int v = tid; v < V; v += NT) {
-      const uint32_t q = key_of(row[v]);
-      if (q > cut.key) above += wt(row[v]);
-      else if (q == cut.key) ++ties;
+  Sampler<RES> sm(sh, row, wt);
+  Cut cut{(float)BINS, 0};
+  if (k > 0 && k < p.vocab) {
+    row.each([&](float x, int) {
+      const float t = wt.t16(x);
+      if (t < (float)BINS) atomicAdd(&sh.hist[(int)t], 1u);
+    });
+    cl.sync();
+    u64 c0, c1, total;
+    sm.pair_counts(c0, c1);
+    const u64 incl = block_scan(c0 + c1, sh.red, total), excl = incl - c0 - c1;
+    if (total > (u64)k) {                                        // else every token that weighs something stays
+      if (excl < (u64)k && (u64)k <= incl) {
+        const bool second = (u64)k > excl + c0;
+        sh.ib[0] = 2 * tid + second;
+        sh.bc[0] = excl + (second ? c0 : 0);
+        sh.bc[1] = second ? c1 : c0;
+      }
+      __syncthreads();
+      const int bin = sh.ib[0];
+      const u64 before = sh.bc[0], in_bin = sh.bc[1];
+      if (before + in_bin == (u64)k) {
+        cut.L = (float)(bin + 1);                                // the bin's end is the border
+        cut.place = ~0ull;
+        cl.sync();
+      } else {
+        row.each([&](float x, int l) {
+          const float t = wt.t16(x);
+          if (t >= (float)bin && t < (float)(bin + 1)) sm.candidate(0, x, l);
+        });
+        cl.sync();
+        uint32_t klo = ~0u, khi = 0;
+        bool all = false;
+        for (int i = 0; i < C; ++i) {
+          klo = min(klo, *cl.map_shared_rank(&sh.kmin[0], i));
+          khi = max(khi, *cl.map_shared_rank(&sh.kmax[0], i));
+          all |= *cl.map_shared_rank(&sh.fcnt[0], i) > LCAP;
+        }
+        const Cut in{(float)bin, 1};                             // (the bin itself is within the places)
+        u64 place = 0;
+        sm.template resolve<false>(0, all, in, (u64)klo << IDX_BITS, ((u64)khi << IDX_BITS) | ((1 << IDX_BITS) - 1), in_bin,
+                                   before, (u64)k, place);
+        cut.L = (float)bin;
+        cut.place = place;
+      }
+    } else {
+      cl.sync();
     }
-    above = block_sum64(above, red);
-    ties = block_sum64(ties, red);
-    const u64 mass = above + min(ties, cut.ties) * wt(of_key(cut.key));
-    const u64 want = (u64)max(1.0, ceil((double)max(top_p, 0.f) * (double)mass));
-    cut = select<true>(row, V, wt, want, hist, sh);
+    if (top_p < 1.f) {
+      for (int i = tid; i < BINS; i += NT) sh.hist[i] = 0;
+      __syncthreads();
+    }
+  }
+  bool summed = false;                                           // sh.wsum holds the kept weight
+  if (top_p < 1.f) {
+    // A bin's weight is counted at 2^-(bin / 16) times 12 bits, interpolated linearly in the
+    // bin: off by less than 4e-4 of it, so bins whose running weight is within 5e-4 of the
+    // border bracket it.
+    const float lim = fminf((float)BINS, cut.L + 1.f);
+    row.each([&](float x, int l) {
+      const float t = wt.t16(x);
+      if (t < lim && cut.holds(t, x, row.index(l))) {
+        const int b = (int)t;
+        atomicAdd(&sh.hist[b], (uint32_t)fmaf(t - (float)b, -173.66f, 4096.5f));
+      }
+    });
+    if (tid < 2) sh.ib[2 + tid] = tid ? BINS - 1 : 0;
+    cl.sync();
+    u64 c0, c1;
+    sm.pair_counts(c0, c1);
+    const float s0 = (float)c0 * exp2f(-(float)(2 * tid) / 16.f), s1 = (float)c1 * exp2f(-(float)(2 * tid + 1) / 16.f);
+    float ftotal;
+    const float fincl = block_scan(s0 + s1, sh.fred, ftotal), fex = fincl - (s0 + s1);
+    // the first bins whose running weight reaches the border less, and plus, the margin
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float b = ftotal * (top_p + (e ? 5e-4f : -5e-4f));
+      const bool hit1 = fex + s0 >= b, hit = fincl >= b;
+      // running sums rise from thread to thread up to their rounding: the lowest hit is taken
+      const unsigned any = __ballot_sync(0xffffffffu, hit && 2 * tid < BINS);
+      if (any && lane == __ffs(any) - 1) sh.red[warp] = (u64)(2 * tid + !hit1);
+      else if (!any && lane == 0) sh.red[warp] = e ? BINS - 1 : BINS;
+      __syncthreads();
+      if (tid == 0) {
+        u64 best = e ? BINS - 1 : BINS;
+        for (int w = NW - 1; w >= 0; --w) best = min(best, sh.red[w]);
+        sh.ib[2 + e] = (int)min(best, (u64)BINS - 1);
+      }
+      __syncthreads();
+    }
+    const float blo = (float)sh.ib[2], bhi = (float)(sh.ib[3] + 1);
+    u64 total = 0, above = 0;
+    row.each([&](float x, int l) {
+      const float t = wt.t16(x);
+      if (t < lim && cut.holds(t, x, row.index(l))) {
+        uint32_t q;
+        int s;
+        wt.parts(x, q, s);
+        total += (u64)q * (u64)(1u << s);
+        if (t < blo) above += (u64)q * (u64)(1u << s);
+        else if (t < bhi) sm.candidate(1, x, l);
+      }
+    });
+    total = warp_sum64(total);
+    above = warp_sum64(above);
+    if (lane == 0) sh.wsum[warp] = above, sh.red[warp] = total;
+    __syncthreads();
+    if (tid == 0) {
+      u64 t = 0, a = 0;
+      for (int w = 0; w < NW; ++w) t += sh.red[w], a += sh.wsum[w];
+      sh.total = t;
+      sh.above = a;
+    }
+    cl.sync();
+    total = above = 0;
+    uint32_t klo = ~0u, khi = 0;
+    u64 n = 0;
+    bool all = false;
+    for (int i = 0; i < C; ++i) {
+      total += *cl.map_shared_rank(&sh.total, i);
+      above += *cl.map_shared_rank(&sh.above, i);
+      klo = min(klo, *cl.map_shared_rank(&sh.kmin[1], i));
+      khi = max(khi, *cl.map_shared_rank(&sh.kmax[1], i));
+      const uint32_t f = *cl.map_shared_rank(&sh.fcnt[1], i);
+      n += f;
+      all |= f > LCAP;
+    }
+    const u64 want = (u64)max(1.0, ceil((double)fmaxf(top_p, 0.f) * (double)total));
+    u64 place = 0;
+    summed = above < want && n > 0 && !all;
+    bool ok = above < want && n > 0 &&
+              sm.template resolve<true>(1, all, cut, (u64)klo << IDX_BITS, ((u64)khi << IDX_BITS) | ((1 << IDX_BITS) - 1), n,
+                                        above, want, place);
+    if (!ok) {                                                   // the bracket missed the border: the whole order
+      cl.sync();
+      if (tid == 0) sh.gcnt[1] = 0;
+      summed = false;
+      __syncthreads();
+      sm.template resolve<true>(1, true, cut, 0, (1ull << (32 + IDX_BITS)) - 1, (u64)p.vocab, 0, want, place);
+    }
+    cut.L = -1.f;                                                // the place alone decides
+    cut.place = place;
   }
   // min-p: (x - m) / T >= ln(min_p)
-  double xmin = -INFINITY;
-  if (min_p > 0.f) xmin = (double)mx + (double)T * log((double)fminf(min_p, 1.f));
-  // the kept weight of each warp's piece of the row; where a tie straddles the cut, its last index
-  const int piece = ((V + NW - 1) / NW + 31) / 32 * 32;
-  const int v0 = warp * piece, v1 = min(V, v0 + piece);
-  u64 ties = 0;
-  for (int v = v0 + lane; v < v1; v += 32) ties += key_of(row[v]) == cut.key;
-  const u64 all_ties = block_sum64(ties, red);
-  int last_tie = V - 1;
-  if (cut.ties < all_ties) {
-    if (tid == 0) {
-      u64 n = 0;
-      for (int v = 0; v < V; ++v)
-        if (key_of(row[v]) == cut.key && ++n == cut.ties) {
-          found = v;
-          break;
-        }
-    }
-    __syncthreads();
-    last_tie = found;
+  float xmin = -INFINITY;
+  if (min_p > 0.f) {
+    xmin = fminf(mx, __double2float_ru((double)mx + (double)T * log((double)fminf(min_p, 1.f))));
   }
-  auto kept = [&](float x, int v) -> u64 {
-    const uint32_t q = key_of(x);
-    if (q < cut.key || (q == cut.key && v > last_tie) || (double)x < xmin) return 0;
+  const bool by_place = cut.place != 0 && cut.place != ~0ull;
+  const float xcut = by_place ? of_key((uint32_t)(cut.place >> IDX_BITS)) : -INFINITY;
+  const float tlim = cut.place == ~0ull ? cut.L : (float)BINS, xlim = fmaxf(xmin, xcut);
+  auto kept = [&](float x, int l) -> u64 {
+    if (!(x >= xlim) || !(wt.t16(x) < tlim)) return 0;
+    if (by_place && x == xcut && place_of(x, row.index(l)) < cut.place) return 0;
     return wt(x);
   };
-  u64 mine = 0;
-  for (int v = v0 + lane; v < v1; v += 32) mine += kept(row[v], v);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-  if (lane == 0) wsum[warp] = mine;
-  __syncthreads();
-  u64 total = 0;
-  for (int w = 0; w < NW; ++w) total += wsum[w];
+  if (summed && xmin <= xcut) {
+    // the weight before the bracket is known: the kept candidates join their pieces
+    for (uint32_t i = tid; i < sh.fcnt[1]; i += NT) {
+      const int l = sh.list[i];
+      const u64 w = kept(row.at(l), l);
+      if (w) atomicAdd(&sh.wsum[(l >> 2) / piece], w);
+    }
+  } else {
+    u64 mine = 0;
+    row.each([&](float x, int l) { mine += kept(x, l); });
+    mine = warp_sum64(mine);
+    __syncthreads();
+    if (lane == 0) sh.wsum[warp] = mine;
+  }
+  cl.sync();
+  const u64 mine = tid < C * NW ? cl.map_shared_rank(&sh.wsum[0], tid / NW)[tid % NW] : 0;
+  u64 total;
+  const u64 incl = block_scan(mine, sh.red, total);
+  cl.barrier_arrive();                                           // the last read of remote shared memory is done
   const float u = p.u[r];
   const double uc = u > 0.f ? fmin((double)u, 1.0 - 0x1p-24) : 0.0;   // NaN: 0
   const u64 target = (u64)(uc * (double)total);
-  u64 base = 0;
-  int w = 0;
-  for (; w < NW - 1 && base + wsum[w] <= target; ++w) base += wsum[w];
-  if (warp != w) return;
-  for (int v = v0; v < v1; v += 32) {
-    const u64 q = v + lane < v1 ? kept(row[v + lane], v + lane) : 0;
-    u64 c = q;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const u64 t = __shfl_up_sync(0xffffffffu, c, o);
-      if (lane >= o) c += t;
-    }
-    const unsigned hit = __ballot_sync(0xffffffffu, base + c > target);
-    if (hit) {
-      const int l = __ffs(hit) - 1;
-      if (lane == l) {
-        p.tokens[(long long)r * p.out_ld] = v + lane;
-        if (p.logprob) {
-          const double x = row[v + lane];
-          const double z = x == (double)mx ? 0.0 : (x - (double)mx) / (double)T;
-          p.logprob[r] = (float)(z - log((double)total * 0x1p-44));
-        }
-      }
-      return;
-    }
-    base += __shfl_sync(0xffffffffu, c, 31);
+  if (mine && incl - mine <= target && target < incl) {
+    sh.ib[0] = tid;
+    sh.bc[0] = incl - mine;
   }
+  __syncthreads();
+  if (sh.ib[0] == rank * NW + warp) {
+    u64 base = sh.bc[0];
+    for (int j0 = row.jb; j0 < row.je; j0 += 32) {
+      const int j = j0 + lane;
+      u64 w[4] = {0, 0, 0, 0};
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (j < row.je) {
+        v = row.quad(j);
+        w[0] = kept(v.x, 4 * j); w[1] = kept(v.y, 4 * j + 1); w[2] = kept(v.z, 4 * j + 2); w[3] = kept(v.w, 4 * j + 3);
+      }
+      const u64 c = warp_scan(w[0] + w[1] + w[2] + w[3]);
+      const unsigned hit = __ballot_sync(0xffffffffu, base + c > target);
+      if (hit) {
+        if (lane == __ffs(hit) - 1) {
+          u64 s = base + c - (w[0] + w[1] + w[2] + w[3]);
+          int e = 0;
+          for (; e < 3; ++e) {
+            s += w[e];
+            if (s > target) break;
+          }
+          const float x = e == 0 ? v.x : e == 1 ? v.y : e == 2 ? v.z : v.w;
+          p.tokens[(long long)r * p.out_ld] = row.index(4 * j + e);
+          if (p.logprob) {
+            const double z = x == mx ? 0.0 : ((double)x - (double)mx) / (double)T;
+            p.logprob[r] = (float)(z - log((double)total * 0x1p-44));
+          }
+        }
+        break;
+      }
+      base += __shfl_sync(0xffffffffu, c, 31);
+    }
+  }
+  cl.barrier_wait();
 }
 
-void launch_sample(const SampleParams& p, cudaStream_t s) {
-  k_sample<<<p.n, NT, 0, s>>>(p);
+// Cluster size: two CTAs on an SM can hold 100 KB of a row each, so that one's passes run while
+// the other loads; with few rows the cluster grows, down to 4096 logits a CTA.
+int launch_sample(const SampleParams& p, cudaStream_t s) {
+  const int quads = p.vocab / 4 + 2;                             // whatever the row's alignment
+  const int sms = device_sm_count();
+  int C = 1;
+  while (C < 8 && ((quads + C - 1) / C > 25200 / 4 || ((long long)p.n * C < sms && quads > C * 2048))) C *= 2;
+  const int chunk = (quads + C - 1) / C;
+  const bool res = (size_t)chunk * 16 + sizeof(Shared) <= 227 * 1024 - 1024;
+  const size_t smem = res ? (size_t)chunk * 16 : 0;
+  const void* kernel = res ? (const void*)k_sample<true> : (const void*)k_sample<false>;
+  if (!ensure_smem_limit(kernel, res ? 227 * 1024 - 1024 - (int)sizeof(Shared) : 0)) return -1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(p.n * (long long)C));
+  cfg.blockDim = dim3(NT);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)C;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  const cudaError_t e = res ? cudaLaunchKernelEx(&cfg, k_sample<true>, p, chunk)
+                            : cudaLaunchKernelEx(&cfg, k_sample<false>, p, chunk);
+  if (e != cudaSuccess) return -1;
   note_launch();
+  return 0;
 }
 
 }  // namespace rdt

@@ -298,6 +298,6 @@ struct SampleParams {
   int* tokens; int out_ld;
   float* logprob;                               // [n] or null
 };
-void launch_sample(const SampleParams& p, cudaStream_t s);
+int launch_sample(const SampleParams& p, cudaStream_t s);
 
 }  // namespace rdt

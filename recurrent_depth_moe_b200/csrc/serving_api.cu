@@ -122,7 +122,7 @@ rdt_status rdt_sample_tokens(const float* logits, long long ld, int n, int vocab
   if (!a.min_p_rows && !(a.min_p >= 0.f && a.min_p <= 1.f)) return RDT_ERR_INVALID_ARG;
   if (n == 0) return RDT_OK;
   if (!logits || !u || !tokens) return RDT_ERR_INVALID_ARG;
-  if (vocab >= (1 << 20)) return RDT_ERR_UNSUPPORTED;   // the 64-bit weight sums hold 2^20 tokens
+  if (vocab >= (1 << 20) || n > (1 << 27)) return RDT_ERR_UNSUPPORTED;   // the 64-bit weight sums hold 2^20 tokens
   cudaStream_t s = (cudaStream_t)stream;
   ProfScope ps(PC_TOKENS, s);
   SampleParams p;
@@ -132,7 +132,7 @@ rdt_status rdt_sample_tokens(const float* logits, long long ld, int n, int vocab
   p.temperature_row = a.temperature_rows; p.top_k_row = a.top_k_rows;
   p.top_p_row = a.top_p_rows; p.min_p_row = a.min_p_rows;
   p.tokens = tokens; p.out_ld = out_ld; p.logprob = logprob;
-  launch_sample(p, s);
+  if (launch_sample(p, s) != 0) return RDT_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? RDT_OK : RDT_ERR_CUDA;
 }
 
