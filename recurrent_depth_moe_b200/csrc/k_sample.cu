@@ -27,6 +27,7 @@
 #include <cooperative_groups.h>
 
 #include <algorithm>
+#include <type_traits>
 
 namespace cg = cooperative_groups;
 
@@ -38,6 +39,7 @@ constexpr int BINS = 46 * 16;    // of the exponent: below 2^-46 a weight rounds
 constexpr int RB = 256;          // bins of one refinement
 constexpr int LCAP = 1024;       // candidates one CTA lists; more are found by passes over the row
 constexpr int IDX_BITS = 20;
+constexpr int CMAX = 8;          // CTAs of a cluster
 typedef unsigned long long u64;
 
 // order of floats as unsigned integers
@@ -68,13 +70,13 @@ struct Weigh {
     i0 = __float_as_int(r);
     nfM = -((Mh - (r - MAGIC)) + (fmaf(mx, chi, -Mh) + mx * clo));
   }
-  // 16 times the exponent, monotone in x; NaN for NaN
-  __device__ __forceinline__ float t16(float x) const { return (m - x) * c16; }
-  // the weight in units of 2^-44 is q << sh; 0 <= t16(x) < BINS
-  __device__ __forceinline__ void parts(float x, uint32_t& q, int& sh) const {
+  // MAGIC plus the bin, 16 times the exponent rounded to a whole number; monotone in x, NaN for NaN
+  __device__ __forceinline__ float bin(float x) const { return fmaf(m - x, c16, MAGIC); }
+  // the weight in units of 2^-44 is q << sh; bin(x) < MAGIC + BINS
+  template <bool WIDE> __device__ __forceinline__ void parts(float x, uint32_t& q, int& sh) const {
     float s;
     int k;
-    if (!wide) {
+    if (!WIDE) {
       const float zh = x * chi, r = zh + MAGIC;
       s = ((zh - (r - MAGIC)) + fmaf(x, clo, nfM)) + fmaf(x, chi, -zh);
       k = i0 - __float_as_int(r);
@@ -87,12 +89,15 @@ struct Weigh {
     }
     const int kk = max(k, 20);
     sh = kk - k;
-    q = __float2uint_rn(exp2f(s) * __int_as_float((171 - kk) << 23));   // 2^(44 - kk)
+    float e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(s));            // -1 <= s <= 1
+    q = __float2uint_rn(e * __int_as_float((171 - kk) << 23));       // 2^(44 - kk)
   }
   __device__ __forceinline__ u64 operator()(float x) const {
     uint32_t q;
     int sh;
-    parts(x, q, sh);
+    if (wide) parts<true>(x, q, sh);
+    else parts<false>(x, q, sh);
     return (u64)q * (u64)(1u << sh);
   }
 };
@@ -148,9 +153,13 @@ template <bool RES> struct Row {
   int V, a, q0, nq;      // the row starts a floats past a 16-byte boundary; quads q0 .. q0 + nq - 1 are this CTA's
   int jb, je;            // this warp's quads, contiguous
   bool inf_row;          // the maximum is +inf: the infinities weigh 1, the rest nothing
+  __device__ __forceinline__ bool full(int j) const {   // the quad lies inside the row
+    const int i = 4 * (q0 + j) - a;
+    return i >= 0 && i + 4 <= V;
+  }
   __device__ __forceinline__ float4 load(int j) const {
     const int i = 4 * (q0 + j) - a;
-    if (i >= 0 && i + 4 <= V) return __ldg(reinterpret_cast<const float4*>(row + i));
+    if (full(j)) return __ldg(reinterpret_cast<const float4*>(row + i));
     const float none = __int_as_float(0x7fffffff);   // past the row's ends: NaN, which takes no part
     float4 v;
     v.x = i >= 0 && i < V ? row[i] : none;
@@ -169,24 +178,33 @@ template <bool RES> struct Row {
   __device__ __forceinline__ float at(int local) const {
     return RES ? reinterpret_cast<const float*>(chunk)[local] : fix(row[index(local)]);
   }
-  // f(x, local index) for every element of the warp's piece, in no order across lanes
-  template <typename F> __device__ __forceinline__ void each(F f) const {
+  // f(four elements, local index of the first) over the warp's piece, in no order across lanes
+  template <typename F> __device__ __forceinline__ void each4(F f) const {
 #pragma unroll 2
     for (int j = jb + (threadIdx.x & 31); j < je; j += 32) {
       const float4 v = quad(j);
-      f(v.x, 4 * j); f(v.y, 4 * j + 1); f(v.z, 4 * j + 2); f(v.w, 4 * j + 3);
+      const float x[4] = {v.x, v.y, v.z, v.w};
+      f(x, 4 * j);
     }
+  }
+  // f(x, local index) for every element of the warp's piece
+  template <typename F> __device__ __forceinline__ void each(F f) const {
+    each4([&](const float* x, int l) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) f(x[e], l + e);
+    });
   }
 };
 
-// Which tokens are in play: bin below L, or in bin L and at or before `place`.
+// Which tokens are in play: bins below L, and of bin L (none: L is BINS) those at or before `place`.
 struct Cut {
-  float L;
+  float L;     // MAGIC + bin
   u64 place;
-  __device__ __forceinline__ bool holds(float t, float x, int v) const {
-    return t < L || (t < L + 1.f && t < (float)BINS && place_of(x, v) >= place);
+  __device__ __forceinline__ bool holds(float b, float x, int v) const {
+    return b < L || (b == L && L < Weigh::MAGIC + BINS && place_of(x, v) >= place);
   }
 };
+__device__ __forceinline__ int bin_index(float b) { return __float_as_int(b) - __float_as_int(Weigh::MAGIC); }
 
 template <bool RES> struct Sampler {
   cg::cluster_group cl;
@@ -201,19 +219,67 @@ template <bool RES> struct Sampler {
   __device__ __forceinline__ void pair_counts(u64& c0, u64& c1) {
     c0 = c1 = 0;
     const int b = 2 * threadIdx.x;
-    if (b < BINS)
-      for (int r = 0; r < C; ++r) {
-        const uint2 h = *reinterpret_cast<const uint2*>(cl.map_shared_rank(sh.hist, r) + b);
-        c0 += h.x;
-        c1 += h.y;
-      }
+    if (b < BINS) {
+      uint2 h[CMAX];                                             // remote reads, all in flight
+#pragma unroll
+      for (int r = 0; r < CMAX; ++r)
+        h[r] = r < C ? *reinterpret_cast<const uint2*>(cl.map_shared_rank(sh.hist, r) + b) : make_uint2(0, 0);
+#pragma unroll
+      for (int r = 0; r < CMAX; ++r) c0 += h[r].x, c1 += h[r].y;
+    }
   }
-  // Note an element as a candidate of phase ph.
-  __device__ __forceinline__ void candidate(int ph, float x, int local) {
-    const uint32_t n = atomicAdd(&sh.fcnt[ph], 1u), k = key_of(x);
-    if (n < LCAP) sh.list[n] = local;
-    atomicMin(&sh.kmin[ph], k);
-    atomicMax(&sh.kmax[ph], k);
+  // One pass over the warp's piece: f(four elements, local index of the first) returns a bit
+  // for each that is a candidate of phase ph.  A lane's bits of eight quads are kept in a
+  // register and listed together.
+  template <typename F> __device__ __forceinline__ void list_each4(int ph, F f) {
+    const int lane = threadIdx.x & 31;
+    uint32_t klo = ~0u, khi = 0;
+    for (int j0 = row.jb; j0 < row.je; j0 += 256) {
+      uint32_t bits = 0;
+#pragma unroll 2
+      for (int e = 0; e < 8; ++e) {
+        const int j = j0 + 32 * e + lane;
+        if (j >= row.je) break;
+        const float4 v = row.quad(j);
+        const float x[4] = {v.x, v.y, v.z, v.w};
+        bits |= f(x, 4 * j) << (4 * e);
+      }
+      __syncwarp();
+      const int c = __popc(bits), incl = warp_scan(c), n = __shfl_sync(0xffffffffu, incl, 31);
+      if (n == 0) continue;
+      uint32_t at = 0;
+      if (lane == 31) at = atomicAdd(&sh.fcnt[ph], (uint32_t)n);
+      at = __shfl_sync(0xffffffffu, at, 31) + incl - c;
+      for (; bits; bits &= bits - 1, ++at) {
+        const int e = __ffs(bits) - 1, l = 4 * (j0 + 32 * (e >> 2) + lane) + (e & 3);
+        const uint32_t k = key_of(row.at(l));
+        klo = min(klo, k);
+        khi = max(khi, k);
+        if (at < LCAP) sh.list[at] = l;
+      }
+      __syncwarp();
+    }
+    klo = __reduce_min_sync(0xffffffffu, klo);
+    khi = __reduce_max_sync(0xffffffffu, khi);
+    if (lane == 0 && klo <= khi) {
+      atomicMin(&sh.kmin[ph], klo);
+      atomicMax(&sh.kmax[ph], khi);
+    }
+  }
+  // The cluster's candidates of phase ph: how many, the range of their places, and whether one
+  // CTA has more than its list holds.
+  __device__ __forceinline__ void range(int ph, u64& n, u64& lo, u64& hi, bool& all) {
+    const int lane = threadIdx.x & 31;
+    uint32_t f = 0, klo = ~0u, khi = 0;
+    if (lane < C) {
+      f = *cl.map_shared_rank(&sh.fcnt[ph], lane);
+      klo = *cl.map_shared_rank(&sh.kmin[ph], lane);
+      khi = *cl.map_shared_rank(&sh.kmax[ph], lane);
+    }
+    n = __reduce_add_sync(0xffffffffu, f);
+    all = __any_sync(0xffffffffu, f > LCAP);
+    lo = (u64)__reduce_min_sync(0xffffffffu, klo) << IDX_BITS;
+    hi = ((u64)__reduce_max_sync(0xffffffffu, khi) << IDX_BITS) | ((1 << IDX_BITS) - 1);
   }
   // f(x, token) for the CTA's candidates of phase ph with places lo .. hi: its list, or
   // (`all`) every element that `in` holds.
@@ -231,7 +297,7 @@ template <bool RES> struct Sampler {
         if (!(x >= xlo)) return;
         const int v = row.index(l);
         const u64 pl = place_of(x, v);
-        if (pl >= lo && pl <= hi && in.holds(wt.t16(x), x, v)) f(x, pl);
+        if (pl >= lo && pl <= hi && in.holds(wt.bin(x), x, v)) f(x, pl);
       });
     }
   }
@@ -256,11 +322,17 @@ template <bool RES> struct Sampler {
       });
       cl.sync();
       u64 c = 0, m = 0;
-      if (threadIdx.x < RB)
-        for (int r = 0; r < C; ++r) {
-          c += cl.map_shared_rank(&sh.cnt[par][0], r)[threadIdx.x];
-          if (MASS) m += cl.map_shared_rank(&sh.mass[par][0], r)[threadIdx.x];
+      if (threadIdx.x < RB) {
+        uint32_t hc[CMAX];
+        u64 hm[CMAX];
+#pragma unroll
+        for (int r = 0; r < CMAX; ++r) {
+          hc[r] = r < C ? cl.map_shared_rank(&sh.cnt[par][0], r)[threadIdx.x] : 0;
+          hm[r] = MASS && r < C ? cl.map_shared_rank(&sh.mass[par][0], r)[threadIdx.x] : 0;
         }
+#pragma unroll
+        for (int r = 0; r < CMAX; ++r) c += hc[r], m += hm[r];
+      }
       if (!MASS) m = c;
       u64 total;
       const u64 incl = block_scan(m, sh.red, total);
@@ -285,13 +357,16 @@ template <bool RES> struct Sampler {
     });
     cl.sync();
     if (threadIdx.x < 32) {
-      u64 pl = 0;
-      int at = threadIdx.x;
-      for (int r = 0; r < C; ++r) {
-        const int g = min(32, (int)*cl.map_shared_rank(&sh.gcnt[ph], r));
-        if (at >= 0 && at < g) pl = cl.map_shared_rank(&sh.glist[ph][0], r)[at];
-        at -= g;
+      const int lane = threadIdx.x;
+      const int g = lane < C ? min(32, (int)*cl.map_shared_rank(&sh.gcnt[ph], lane)) : 0;
+      int at = lane, from = -1, i = 0;
+#pragma unroll
+      for (int r = 0; r < CMAX; ++r) {
+        const int gr = __shfl_sync(0xffffffffu, g, r);
+        if (at >= 0 && at < gr) from = r, i = at;
+        at -= gr;
       }
+      const u64 pl = from >= 0 ? cl.map_shared_rank(&sh.glist[ph][0], from)[i] : 0;
       u64 w = 0, before = base;
       if (pl) w = MASS ? wt(of_key((uint32_t)(pl >> IDX_BITS))) : 1;
 #pragma unroll
@@ -341,12 +416,17 @@ __global__ void __launch_bounds__(NT, 2) k_sample(SampleParams p, int chunk_quad
   if (tid < 2) sh.fcnt[tid] = sh.gcnt[tid] = sh.kmax[tid] = 0, sh.kmin[tid] = ~0u;
   if (tid == 0) sh.idx = 0x7fffffff;
   float mx = -INFINITY;
-#pragma unroll 4
-  for (int j = row.jb + lane; j < row.je; j += 32) {
-    const float4 v = row.load(j);
-    if (RES) chunk[j] = v;
-    mx = fmaxf(fmaxf(mx, fmaxf(v.x, v.y)), fmaxf(v.z, v.w));   // fmaxf drops NaN
+  if (RES) {                                                     // the whole piece is in flight at once
+    for (int j = row.jb + lane; j < row.je; j += 32) {
+      if (row.full(j))
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(chunk + j)),
+                     "l"(row.row + row.index(4 * j)));
+      else
+        chunk[j] = row.load(j);
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");             // each lane reads its own quads back
   }
+  row.each([&](float x, int) { mx = fmaxf(mx, x); });            // fmaxf drops NaN
   mx = warp_max(mx);
   if (lane == 0) sh.fred[warp] = mx;
   __syncthreads();
@@ -380,11 +460,12 @@ __global__ void __launch_bounds__(NT, 2) k_sample(SampleParams p, int chunk_quad
   }
   const Weigh wt(mx, T);
   Sampler<RES> sm(sh, row, wt);
-  Cut cut{(float)BINS, 0};
+  constexpr float MAGIC = Weigh::MAGIC;
+  Cut cut{MAGIC + BINS, 0};
   if (k > 0 && k < p.vocab) {
     row.each([&](float x, int) {
-      const float t = wt.t16(x);
-      if (t < (float)BINS) atomicAdd(&sh.hist[(int)t], 1u);
+      const float b = wt.bin(x);
+      if (b < MAGIC + BINS) atomicAdd(&sh.hist[bin_index(b)], 1u);
     });
     cl.sync();
     u64 c0, c1, total;
@@ -401,27 +482,24 @@ __global__ void __launch_bounds__(NT, 2) k_sample(SampleParams p, int chunk_quad
       const int bin = sh.ib[0];
       const u64 before = sh.bc[0], in_bin = sh.bc[1];
       if (before + in_bin == (u64)k) {
-        cut.L = (float)(bin + 1);                                // the bin's end is the border
+        cut.L = MAGIC + (float)(bin + 1);                        // the bin's end is the border
         cut.place = ~0ull;
         cl.sync();
       } else {
-        row.each([&](float x, int l) {
-          const float t = wt.t16(x);
-          if (t >= (float)bin && t < (float)(bin + 1)) sm.candidate(0, x, l);
+        sm.list_each4(0, [&](const float* x, int) {
+          uint32_t bits = 0;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) bits |= (uint32_t)(wt.bin(x[e]) == MAGIC + (float)bin) << e;
+          return bits;
         });
         cl.sync();
-        uint32_t klo = ~0u, khi = 0;
-        bool all = false;
-        for (int i = 0; i < C; ++i) {
-          klo = min(klo, *cl.map_shared_rank(&sh.kmin[0], i));
-          khi = max(khi, *cl.map_shared_rank(&sh.kmax[0], i));
-          all |= *cl.map_shared_rank(&sh.fcnt[0], i) > LCAP;
-        }
-        const Cut in{(float)bin, 1};                             // (the bin itself is within the places)
+        u64 n, lo, hi;
+        bool all;
+        sm.range(0, n, lo, hi, all);
+        const Cut in{MAGIC + (float)bin, 0};                     // (the places leave only the bin itself)
         u64 place = 0;
-        sm.template resolve<false>(0, all, in, (u64)klo << IDX_BITS, ((u64)khi << IDX_BITS) | ((1 << IDX_BITS) - 1), in_bin,
-                                   before, (u64)k, place);
-        cut.L = (float)bin;
+        sm.template resolve<false>(0, all, in, lo, hi, n, before, (u64)k, place);
+        cut.L = MAGIC + (float)bin;
         cut.place = place;
       }
     } else {
@@ -434,15 +512,15 @@ __global__ void __launch_bounds__(NT, 2) k_sample(SampleParams p, int chunk_quad
   }
   bool summed = false;                                           // sh.wsum holds the kept weight
   if (top_p < 1.f) {
-    // A bin's weight is counted at 2^-(bin / 16) times 12 bits, interpolated linearly in the
-    // bin: off by less than 4e-4 of it, so bins whose running weight is within 5e-4 of the
-    // border bracket it.
-    const float lim = fminf((float)BINS, cut.L + 1.f);
+    // A weight is counted as 12 bits of 2^-(bin / 16), interpolated linearly in the bin (up to
+    // half a bin to each side): off by less than 4e-4 of it, so bins whose running weight is
+    // within 5e-4 of the border bracket it.
+    const float lim = fminf(MAGIC + (BINS - 1), cut.L);
     row.each([&](float x, int l) {
-      const float t = wt.t16(x);
-      if (t < lim && cut.holds(t, x, row.index(l))) {
-        const int b = (int)t;
-        atomicAdd(&sh.hist[b], (uint32_t)fmaf(t - (float)b, -173.66f, 4096.5f));
+      const float b = wt.bin(x);
+      if (b <= lim && (b < cut.L || cut.holds(b, x, row.index(l)))) {
+        const float f = fmaf(wt.m - x, wt.c16, -(b - MAGIC));
+        atomicAdd(&sh.hist[bin_index(b)], __float_as_uint(fmaf(f, -177.45f, 4096.f + 8388608.f)) & 0x3fffu);
       }
     });
     if (tid < 2) sh.ib[2 + tid] = tid ? BINS - 1 : 0;
@@ -469,19 +547,36 @@ __global__ void __launch_bounds__(NT, 2) k_sample(SampleParams p, int chunk_quad
       }
       __syncthreads();
     }
-    const float blo = (float)sh.ib[2], bhi = (float)(sh.ib[3] + 1);
+    const float blo = MAGIC + (float)sh.ib[2], bhi = MAGIC + (float)sh.ib[3];
     u64 total = 0, above = 0;
-    row.each([&](float x, int l) {
-      const float t = wt.t16(x);
-      if (t < lim && cut.holds(t, x, row.index(l))) {
-        uint32_t q;
-        int s;
-        wt.parts(x, q, s);
-        total += (u64)q * (u64)(1u << s);
-        if (t < blo) above += (u64)q * (u64)(1u << s);
-        else if (t < bhi) sm.candidate(1, x, l);
-      }
-    });
+    auto weigh = [&](auto wide) {
+      sm.list_each4(1, [&](const float* x, int l) {
+        float b[4];
+        bool any = false;
+        uint32_t bits = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          b[e] = wt.bin(x[e]);
+          any |= b[e] <= lim;
+        }
+        if (!any) return bits;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          uint32_t q;
+          int s;
+          wt.template parts<decltype(wide)::value>(x[e], q, s);
+          if (!(b[e] <= lim)) q = 0;
+          if (b[e] == cut.L && !cut.holds(b[e], x[e], row.index(l + e))) q = 0;
+          const u64 f = 1u << s;
+          total += (u64)q * f;
+          above += (u64)(b[e] < blo ? q : 0) * f;
+          bits |= (uint32_t)(b[e] >= blo && b[e] <= bhi && q) << e;
+        }
+        return bits;
+      });
+    };
+    if (wt.wide) weigh(std::true_type());
+    else weigh(std::false_type());
     total = warp_sum64(total);
     above = warp_sum64(above);
     if (lane == 0) sh.wsum[warp] = above, sh.red[warp] = total;
@@ -493,25 +588,16 @@ __global__ void __launch_bounds__(NT, 2) k_sample(SampleParams p, int chunk_quad
       sh.above = a;
     }
     cl.sync();
-    total = above = 0;
-    uint32_t klo = ~0u, khi = 0;
-    u64 n = 0;
-    bool all = false;
-    for (int i = 0; i < C; ++i) {
-      total += *cl.map_shared_rank(&sh.total, i);
-      above += *cl.map_shared_rank(&sh.above, i);
-      klo = min(klo, *cl.map_shared_rank(&sh.kmin[1], i));
-      khi = max(khi, *cl.map_shared_rank(&sh.kmax[1], i));
-      const uint32_t f = *cl.map_shared_rank(&sh.fcnt[1], i);
-      n += f;
-      all |= f > LCAP;
-    }
+    total = warp_sum64(lane < C ? *cl.map_shared_rank(&sh.total, lane) : 0);
+    above = warp_sum64(lane < C ? *cl.map_shared_rank(&sh.above, lane) : 0);
+    u64 n, lo, hi;
+    bool all;
+    sm.range(1, n, lo, hi, all);
     const u64 want = (u64)max(1.0, ceil((double)fmaxf(top_p, 0.f) * (double)total));
     u64 place = 0;
     summed = above < want && n > 0 && !all;
     bool ok = above < want && n > 0 &&
-              sm.template resolve<true>(1, all, cut, (u64)klo << IDX_BITS, ((u64)khi << IDX_BITS) | ((1 << IDX_BITS) - 1), n,
-                                        above, want, place);
+              sm.template resolve<true>(1, all, cut, lo, hi, n, above, want, place);
     if (!ok) {                                                   // the bracket missed the border: the whole order
       cl.sync();
       if (tid == 0) sh.gcnt[1] = 0;
@@ -529,12 +615,11 @@ __global__ void __launch_bounds__(NT, 2) k_sample(SampleParams p, int chunk_quad
   }
   const bool by_place = cut.place != 0 && cut.place != ~0ull;
   const float xcut = by_place ? of_key((uint32_t)(cut.place >> IDX_BITS)) : -INFINITY;
-  const float tlim = cut.place == ~0ull ? cut.L : (float)BINS, xlim = fmaxf(xmin, xcut);
-  auto kept = [&](float x, int l) -> u64 {
-    if (!(x >= xlim) || !(wt.t16(x) < tlim)) return 0;
-    if (by_place && x == xcut && place_of(x, row.index(l)) < cut.place) return 0;
-    return wt(x);
+  const float blim = cut.place == ~0ull ? cut.L : MAGIC + BINS, xlim = fmaxf(xmin, xcut);
+  auto keeps = [&](float x, int l) {
+    return x >= xlim && wt.bin(x) < blim && !(by_place && x == xcut && place_of(x, row.index(l)) < cut.place);
   };
+  auto kept = [&](float x, int l) -> u64 { return keeps(x, l) ? wt(x) : 0; };
   if (summed && xmin <= xcut) {
     // the weight before the bracket is known: the kept candidates join their pieces
     for (uint32_t i = tid; i < sh.fcnt[1]; i += NT) {
@@ -544,7 +629,23 @@ __global__ void __launch_bounds__(NT, 2) k_sample(SampleParams p, int chunk_quad
     }
   } else {
     u64 mine = 0;
-    row.each([&](float x, int l) { mine += kept(x, l); });
+    auto weigh = [&](auto wide) {
+      row.each4([&](const float* x, int l) {
+        bool in[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) in[e] = keeps(x[e], l + e);
+        if (!(in[0] | in[1] | in[2] | in[3])) return;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          uint32_t q;
+          int s;
+          wt.template parts<decltype(wide)::value>(x[e], q, s);
+          mine += (u64)(in[e] ? q : 0) * (u64)(1u << s);
+        }
+      });
+    };
+    if (wt.wide) weigh(std::true_type());
+    else weigh(std::false_type());
     mine = warp_sum64(mine);
     __syncthreads();
     if (lane == 0) sh.wsum[warp] = mine;
@@ -603,7 +704,7 @@ int launch_sample(const SampleParams& p, cudaStream_t s) {
   const int quads = p.vocab / 4 + 2;                             // whatever the row's alignment
   const int sms = device_sm_count();
   int C = 1;
-  while (C < 8 && ((quads + C - 1) / C > 25200 / 4 || ((long long)p.n * C < sms && quads > C * 2048))) C *= 2;
+  while (C < CMAX && ((quads + C - 1) / C > 25200 / 4 || ((long long)p.n * C < sms && quads > C * 2048))) C *= 2;
   const int chunk = (quads + C - 1) / C;
   const bool res = (size_t)chunk * 16 + sizeof(Shared) <= 227 * 1024 - 1024;
   const size_t smem = res ? (size_t)chunk * 16 : 0;
