@@ -1,13 +1,27 @@
 // One-token attention over the paged key / value cache (GQA): for query head h of sequence b
 //   o = sum_j softmax_j(q . k_j / sqrt(hd)) v_j,   j < the sequence's visible keys,
-// zero where nothing is visible.  The keys of a sequence are split into n_split ranges of its
-// own length, each with a running maximum m and sum l (base-2 logarithms); the ranges are
-// joined by  o = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s.
+// zero where nothing is visible.  Every cached byte is read once (per 8 query heads of a kv
+// head), so the floor is the cache's bytes at HBM rate.
 //
-// k_paged_attn_any: any head width up to 256, any page size, fp32 or bf16, both storage forms.
-// CTA = (range, kv head and tile of 8 of its query heads, sequence); 32-key K and V tiles are
-// widened to fp32 in shared memory, a warp scores its heads with a key per lane, and a thread
-// sums its output channels.  Everything is held in fp32.
+// The work is one line of tiles: (sequence, kv head and group of 8 query heads, keys).  The
+// grid is what the GPU holds at once, and its i-th worker takes the i-th equal piece of the
+// line, so ragged lengths and any batch keep every worker busy to the end; the lengths stay on
+// the device.  A worker walks its piece with the running maximum m and sum l of a softmax
+// (base-2 logarithms).  A (sequence, head group) that one worker walks whole is written at
+// once; where it is spread over several, k_paged_attn_join joins their parts,
+//   o = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s.
+//
+// k_paged_attn_mma (bf16 model, either storage, head width a multiple of 8 (16 for e4m3) up to
+// 256): both products on mma.m16n8k16 with the query heads as the 16 rows.  The cache moves by
+// 16-byte cp.async into a ring that each warp keeps for itself, so no warp waits for another.
+// Fragments are read with 16-byte loads under a permutation of the channels (scores) and of the
+// keys (values), the same on both operands, and a xor of the 16-byte pieces by row keeps those
+// loads free of bank conflicts.  A weight p enters the second product in two 16-bit words: rows
+// 0-7 hold its upper, rows 8-15 its lower word, which the 8 heads leave free, so p has 16 (bf16)
+// or 22 (fp16) bits at no cost.  e4m3 values become fp16, exactly; a row's exponent of K scales
+// its score, of V its weight, relative to the largest exponent so far.
+//
+// k_paged_attn_simt (fp32 model, other widths): a lane per key and per channel in fp32.
 #include "paged.cuh"
 
 #include <algorithm>
@@ -15,187 +29,797 @@
 namespace rdt {
 
 namespace {
-constexpr int TK = 32, GT = 8;   // keys and query heads per tile
-inline size_t any_smem(int hd) { return sizeof(float) * ((size_t)GT * hd + 2 * (size_t)TK * (hd + 1) + GT * TK + GT) + 2 * TK * sizeof(long long); }
+constexpr int GT = 8;               // query heads of a group
+constexpr int WARPS = 4;            // of a CTA
+constexpr float LOG2E = 1.4426950408889634f;
+
+__device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// ------------------------------------------------------------------------------------------
+// the line of work
+// ------------------------------------------------------------------------------------------
+// Units per sequence: ceil(keys / tile) tiles for each of `segs` (kv head, head group) pairs.
+__device__ __forceinline__ int tiles_of(const PagedAttnParams& p, int b, int tile) {
+  return (visible_keys(p.c, p.lens, b, p.len_add, p.st, 221) + tile - 1) / tile;
+}
+// Length of the line (all 128 threads of the CTA; red: 4 words of shared memory).
+__device__ long long line_length(const PagedAttnParams& p, int segs, int tile, long long* red) {
+  long long n = 0;
+  for (int b = threadIdx.x; b < p.B; b += 128) n += (long long)tiles_of(p, b, tile) * segs;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = n;
+  __syncthreads();
+  return red[0] + red[1] + red[2] + red[3];
+}
+// The sequence that holds unit x, and x's place in it, by one warp: 32 sequences at a time.
+struct Place {
+  int b;
+  long long at;
+};
+__device__ __forceinline__ Place line_find(const PagedAttnParams& p, int segs, int tile, long long x) {
+  const int lane = threadIdx.x & 31;
+  long long base = 0;
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    const int b = b0 + lane;
+    const long long n = b < p.B ? (long long)tiles_of(p, b, tile) * segs : 0;
+    long long c = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long t = __shfl_up_sync(0xffffffffu, c, o);
+      if (lane >= o) c += t;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, base + c > x);
+    if (hit) {
+      const int l = __ffs(hit) - 1;
+      return Place{b0 + l, x - base - __shfl_sync(0xffffffffu, c - n, l)};
+    }
+    base += __shfl_sync(0xffffffffu, c, 31);
+  }
+  return Place{p.B, 0};
+}
+// Units of a worker: an equal share, but no less than `least` (a short line is not spread thin).
+__device__ __forceinline__ long long piece_of(long long length, int workers, int least) {
+  const long long q = (length + workers - 1) / workers;
+  return q > least ? q : least;
+}
+
+// ------------------------------------------------------------------------------------------
+// parts of a head group: m, l per head and o per head and channel, fp32
+// ------------------------------------------------------------------------------------------
+// Worker i leaves part 0 of the group it enters in the middle and part 1 of the one it begins
+// and does not finish, and in desc[i] the group it enters in the middle and finishes: it is the
+// last of the workers first .. i that share it.
+struct Desc {
+  int b, seg, first, pad;
+};
+__device__ __forceinline__ float* part_ml(const PagedAttnParams& p, int worker, int which) {
+  return p.part_ml + ((long long)worker * 2 + which) * GT * 2;
+}
+__device__ __forceinline__ float* part_o(const PagedAttnParams& p, int worker, int which) {
+  return p.part_o + ((long long)worker * 2 + which) * GT * p.c.hd;
+}
+__device__ __forceinline__ Desc* desc_of(const PagedAttnParams& p) { return reinterpret_cast<Desc*>(p.scratch); }
+__device__ __forceinline__ void zero_rows(const PagedAttnParams& p, int tile, int es) {
+  const int n = p.H * p.c.hd * es / 2;   // 16-bit words of a row
+  for (int b = blockIdx.x; b < p.B; b += gridDim.x)
+    if (tiles_of(p, b, tile) == 0)
+      for (int i = threadIdx.x; i < n; i += 128) ((uint16_t*)p.o)[(long long)b * p.o_row * es / 2 + i] = 0;
+}
+__device__ __forceinline__ void let_join_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+}  // namespace
+
+// ------------------------------------------------------------------------------------------
+// tensor-core kernel
+// ------------------------------------------------------------------------------------------
+namespace {
+// Keys of a tile and ring stages: K and V of a tile are 8 KB at 128 channels.
+template <bool Q> struct Tile { static constexpr int KEYS = Q ? 32 : 16; };
+constexpr int STAGES = 3;
+
+template <int HD, bool Q> struct Ring {    // HD: the head width rounded up to 64, 128 or 256
+  static constexpr int ROW = HD * (Q ? 1 : 2);                  // bytes of a row
+  static constexpr int STAGE = 2 * Tile<Q>::KEYS * ROW;         // K then V
+  static constexpr int BYTES = STAGES * STAGE;                  // of a warp
+};
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool valid) {
+  const int n = valid ? 16 : 0;                                 // 0: zeros are written, nothing is read
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n));
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+template <bool Q>
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  if (Q)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t e4m3x2_h2(uint32_t two) {   // two e4m3 bytes to fp16, exactly
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((unsigned short)two));
+  return r;
+}
+// Two weights as 16-bit words: the upper ones packed, and what they leave.
+template <bool Q> __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
+  if (Q) {
+    const __half2 h = __floats2half2_rn(x, y);
+    const float2 f = __half22float2(h);
+    const __half2 l = __floats2half2_rn(x - f.x, y - f.y);
+    hi = *reinterpret_cast<const uint32_t*>(&h);
+    lo = *reinterpret_cast<const uint32_t*>(&l);
+  } else {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+    const float2 f = __bfloat1622float2(h);
+    const __nv_bfloat162 l = __floats2bfloat162_rn(x - f.x, y - f.y);
+    hi = *reinterpret_cast<const uint32_t*>(&h);
+    lo = *reinterpret_cast<const uint32_t*>(&l);
+  }
+}
+// 16-byte piece c of row r of a K tile: the 8 lanes of one 16-byte load phase hold rows 2i,
+// 2i + 1 and 4 neighbouring pieces; of a V tile: rows 2i (+ const), i < 4, and pieces 2j, 2j + 1.
+// Rows of 4 pieces (64 e4m3 channels) lie two to a 128-byte line: K needs no xor, and half the
+// conflicts of V remain.
+template <int PIECES> __device__ __forceinline__ int swz_k(int r, int c) {
+  return PIECES < 8 ? c : c ^ ((r & 1) << 2 | (r >> 1 & 3));
+}
+template <int PIECES> __device__ __forceinline__ int swz_v(int r, int c) {
+  return c ^ (PIECES < 8 ? (r >> 1 & 1) << 1 : (r >> 1 & 3) << 1);
+}
+}  // namespace
+
+// 2^d, d <= 0; below the smallest normal value: nothing
+__device__ __forceinline__ float pow2_down(int d) { return d < -126 ? 0.f : __int_as_float((127 + d) << 23); }
+
+template <int HD, bool Q>
+__global__ void __launch_bounds__(32 * WARPS, HD <= 128 ? 2 : 1) k_paged_attn_mma(PagedAttnParams p, int least) {
+  constexpr int KEYS = Tile<Q>::KEYS, ROW = Ring<HD, Q>::ROW, STAGE = Ring<HD, Q>::STAGE;
+  constexpr int NG = KEYS / 8;                        // groups of 8 keys
+  constexpr int PIECES = ROW / 16, EPP = Q ? 16 : 8;  // 16-byte pieces of a row, elements of a piece
+  constexpr int QR = HD / 16;                         // k16 steps of a score
+  constexpr int VH = (PIECES + 7) / 8;                // pieces of a value row that one lane reads
+  constexpr int NC = VH * EPP;                        // groups of 8 channels
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ long long red[WARPS];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, j4 = lane & 3, n8 = lane >> 2;
+  const int hd = p.c.hd, Hkv = p.c.Hkv, G = p.H / Hkv, n_ht = (G + GT - 1) / GT, segs = Hkv * n_ht;
+  const int ps = p.c.page_size, row_bytes = hd * (Q ? 1 : 2), pieces = row_bytes / 16;
+  const bool vec_o = !(((uintptr_t)p.o | (uintptr_t)(p.o_row * 2)) & 15) && hd % 8 == 0;
+  zero_rows(p, KEYS, 2);
+  const long long length = line_length(p, segs, KEYS, red);
+  const int worker = blockIdx.x * WARPS + warp;
+  const long long piece = piece_of(length, gridDim.x * WARPS, least);
+  const long long w0 = worker * piece, w1 = w0 + piece < length ? w0 + piece : length;
+  unsigned char* ring = smem + warp * Ring<HD, Q>::BYTES;
+  const uint32_t ring_a = smem_addr(ring);
+  // the pieces past the head's width hold zeros
+  if (pieces < PIECES)
+    for (int i = lane; i < Ring<HD, Q>::BYTES / 16; i += 32) reinterpret_cast<uint4*>(ring)[i] = make_uint4(0, 0, 0, 0);
+  __syncwarp();
+  Desc joins{-1, 0, 0, 0};
+  Place at = w0 < w1 ? line_find(p, segs, KEYS, w0) : Place{0, 0};
+  for (long long x = w0; x < w1;) {
+    // ---- one (sequence, head group): tiles t0 .. t1 - 1 of its nt
+    const int b = at.b, len = visible_keys(p.c, p.lens, b, p.len_add, nullptr, 0), nt = (len + KEYS - 1) / KEYS;
+    if (at.at >= (long long)nt * segs) {
+      at = Place{b + 1, 0};
+      continue;
+    }
+    const int seg = (int)(at.at / nt), t0 = (int)(at.at % nt);
+    const int t1 = nt - t0 < w1 - x ? nt : t0 + (int)(w1 - x);
+    const int g = seg / n_ht, h0 = seg % n_ht * GT, nh = min(GT, G - h0);
+    float m = -INFINITY, l = 0.f;                     // of head n8; l: this lane's keys
+    float acc[NC][4];                                 // [channel group]: rows n8 (upper words), n8 + 8 (lower)
+    uint32_t qf[QR][2];                               // the query's fragments: row n8, columns of the two k8 halves
+    int vexp = -128;                                  // e4m3: acc is in units of 2^vexp
+    float sl2;                                        // scores to base-2 logarithms (and the query's own scale)
+    // the query
+    {
+      const bf16* q = (const bf16*)p.q + (long long)b * p.q_row + (long long)(g * G + h0 + n8) * hd;
+      float qmax = 0.f;
+      if (Q) {
+        if (n8 < nh)
+          for (int d = j4; d < hd; d += 4) qmax = fmaxf(qmax, finite_abs(to_f(q[d])));
+        qmax = fmaxf(qmax, __shfl_xor_sync(0xffffffffu, qmax, 1));
+        qmax = fmaxf(qmax, __shfl_xor_sync(0xffffffffu, qmax, 2));
+      }
+      // e4m3: the query becomes fp16 with its largest magnitude in [2^14, 2^15), which leaves
+      // out only what is 2^39 smaller
+      int qe = 0;
+      if (Q && qmax > 0.f) {
+        frexpf(qmax, &qe);
+        qe = 15 - qe;
+      }
+      const float qs = Q ? ldexpf(1.f, min(qe, 126)) : 1.f;
+      sl2 = p.scale * LOG2E / qs;
+      // channel of (piece round i, k16 step u, half, pair): lane j4 of a row holds piece 4 i + j4
+#pragma unroll
+      for (int s = 0; s < QR; ++s)
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          const int per = EPP / 4;                    // k16 steps of a round
+          const int d = ((s / per) * 4 + j4) * EPP + (s % per) * 4 + hf * 2;
+          float x = 0.f, y = 0.f;
+          if (n8 < nh && d < hd) x = to_f(q[d]), y = to_f(q[d + 1]);
+          if (Q) {
+            const __half2 h = __floats2half2_rn(x * qs, y * qs);
+            qf[s][hf] = *reinterpret_cast<const uint32_t*>(&h);
+          } else {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+            qf[s][hf] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < NC; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+
+    // ---- the cache's tiles, two ahead.  Lane r holds the slot of key r of the tile to issue.
+    auto slot_of = [&](int t) -> long long {
+      const int key = t * KEYS + lane;
+      if (lane >= KEYS || t >= t1 || key >= len) return -1;
+      const int page = page_of(p.c, b, key, p.st, 222);
+      return page < 0 ? -1 : ((long long)page * Hkv + g) * ps + key % ps;
+    };
+    long long slot_n = slot_of(t0);                   // of the next tile to issue
+    int ke_r[STAGES], ve_r[STAGES];                   // e4m3: exponents of lane's key, by stage (rotated)
+    unsigned ok_r[STAGES];                            // keys of a stage that take part
+#pragma unroll
+    for (int i = 0; i < STAGES; ++i) ke_r[i] = ve_r[i] = 0, ok_r[i] = 0;
+    auto issue = [&](int t, int st, int& ke, int& ve, unsigned& ok) {
+      const long long slot = slot_n;
+      ok = __ballot_sync(0xffffffffu, slot >= 0);
+      if (t < t1) {
+        const uint32_t ka = ring_a + st * STAGE, va = ka + KEYS * ROW;
+        // each row's pieces by neighbouring lanes
+#pragma unroll
+        for (int i0 = 0; i0 < KEYS * PIECES; i0 += 32) {
+          const int i = i0 + lane, r = i / PIECES, c = i % PIECES;
+          const long long s = __shfl_sync(0xffffffffu, slot, r);
+          if (c < pieces) {
+            const long long off = s >= 0 ? s * row_bytes + c * 16 : 0;
+            cp16(ka + r * ROW + swz_k<PIECES>(r, c) * 16, (const char*)p.c.k + off, s >= 0);
+            cp16(va + r * ROW + swz_v<PIECES>(r, c) * 16, (const char*)p.c.v + off, s >= 0);
+          }
+        }
+        if (Q && slot >= 0) {
+          ke = __ldg(p.c.ke + slot);
+          ve = __ldg(p.c.ve + slot);
+        }
+      }
+      cp_commit();
+      slot_n = slot_of(t + 1);
+    };
+#pragma unroll
+    for (int i = 0; i < STAGES - 1; ++i) issue(t0 + i, i, ke_r[i], ve_r[i], ok_r[i]);
+    for (int tb = t0; tb < t1; tb += STAGES) {
+#pragma unroll
+      for (int st = 0; st < STAGES; ++st) {
+        const int t = tb + st;
+        if (t >= t1) break;
+        issue(t + STAGES - 1, (st + STAGES - 1) % STAGES, ke_r[(st + STAGES - 1) % STAGES], ve_r[(st + STAGES - 1) % STAGES],
+              ok_r[(st + STAGES - 1) % STAGES]);
+        cp_wait<STAGES - 1>();
+        __syncwarp();
+        const uint32_t ka = ring_a + st * STAGE, va = ka + KEYS * ROW;
+        const unsigned ok = ok_r[st];
+        // scores of head n8, keys 8 g + 2 j4, + 1
+        float sc[NG][4];
+#pragma unroll
+        for (int kg = 0; kg < NG; ++kg) {
+          sc[kg][0] = sc[kg][1] = sc[kg][2] = sc[kg][3] = 0.f;
+          const int r = kg * 8 + n8;
+#pragma unroll
+          for (int i = 0; i < (PIECES + 3) / 4; ++i) {
+            const uint4 v = lds16(ka + r * ROW + swz_k<PIECES>(r, 4 * i + j4) * 16);
+            if (!Q) {
+              mma<Q>(sc[kg], qf[2 * i][0], 0u, qf[2 * i][1], 0u, v.x, v.y);
+              mma<Q>(sc[kg], qf[2 * i + 1][0], 0u, qf[2 * i + 1][1], 0u, v.z, v.w);
+            } else {
+              const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+              for (int u = 0; u < 4; ++u)
+                mma<Q>(sc[kg], qf[4 * i + u][0], 0u, qf[4 * i + u][1], 0u, e4m3x2_h2(w[u] & 0xffff), e4m3x2_h2(w[u] >> 16));
+            }
+          }
+        }
+        float mx = -INFINITY;
+#pragma unroll
+        for (int kg = 0; kg < NG; ++kg)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int r = kg * 8 + 2 * j4 + e;
+            float f = sl2;
+            if (Q) f *= exp_byte_scale(__shfl_sync(0xffffffffu, ke_r[st], r));
+            const float s = (ok >> r & 1) ? sc[kg][e] * f : -INFINITY;
+            sc[kg][e] = s;
+            mx = s > mx || s != s ? s : mx;             // a NaN score makes the row NaN
+          }
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const float mn = fmaxf(m, mx), base = mn == -INFINITY ? 0.f : mn;
+        float corr = ex2(m - base);
+        m = mn;
+        int ve_max = vexp;
+        if (Q) ve_max = max(vexp, (int)__reduce_max_sync(0xffffffffu, (ok >> lane & 1) ? ve_r[st] : -1) - 127);
+        const float shrink = Q ? pow2_down(vexp - ve_max) : 1.f;
+        vexp = ve_max;
+        if (__any_sync(0xffffffffu, corr != 1.f || shrink != 1.f)) {
+          const float f = corr * shrink;
+#pragma unroll
+          for (int i = 0; i < NC; ++i) acc[i][0] *= f, acc[i][1] *= f, acc[i][2] *= f, acc[i][3] *= f;
+        }
+        l *= corr;
+        uint32_t ph[NG], pl[NG];                        // weights of keys 8 g + 2 j4, + 1
+#pragma unroll
+        for (int kg = 0; kg < NG; ++kg) {
+          float w[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float x = ex2(sc[kg][e] - base);
+            l += x;                                     // this lane's keys; the 4 lanes are summed at the end
+            w[e] = x;
+            if (Q) {
+              const int r = kg * 8 + 2 * j4 + e;
+              const int ve = __shfl_sync(0xffffffffu, ve_r[st], r);
+              w[e] = (ok >> r & 1) ? x * pow2_down(ve - 127 - vexp) : 0.f;
+            }
+          }
+          split2<Q>(w[0], w[1], ph[kg], pl[kg]);
+        }
+        // values: lane holds keys 2 j4, + 1 of two groups, pieces n8 (+ 8) of their rows
+#pragma unroll
+        for (int kk = 0; kk < NG; kk += 2)
+#pragma unroll
+          for (int h = 0; h < VH; ++h) {
+            {
+              // (e4m3 rows of 64 have 4 pieces: the upper lanes' channels do not exist)
+              const int cc = PIECES % 8 ? (h * 8 + n8) % PIECES : h * 8 + n8, r = kk * 8 + 2 * j4;
+              const uint4 v0 = lds16(va + r * ROW + swz_v<PIECES>(r, cc) * 16), v1 = lds16(va + (r + 1) * ROW + swz_v<PIECES>(r + 1, cc) * 16);
+              const uint4 v2 = lds16(va + (r + 8) * ROW + swz_v<PIECES>(r + 8, cc) * 16), v3 = lds16(va + (r + 9) * ROW + swz_v<PIECES>(r + 9, cc) * 16);
+              const uint32_t x0[4] = {v0.x, v0.y, v0.z, v0.w}, x1[4] = {v1.x, v1.y, v1.z, v1.w};
+              const uint32_t x2[4] = {v2.x, v2.y, v2.z, v2.w}, x3[4] = {v3.x, v3.y, v3.z, v3.w};
+              if (!Q) {
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {           // channels 2 u, 2 u + 1 of the piece
+                  mma<Q>(acc[h * 8 + 2 * u], ph[kk], pl[kk], ph[kk + 1], pl[kk + 1], __byte_perm(x0[u], x1[u], 0x5410),
+                         __byte_perm(x2[u], x3[u], 0x5410));
+                  mma<Q>(acc[h * 8 + 2 * u + 1], ph[kk], pl[kk], ph[kk + 1], pl[kk + 1], __byte_perm(x0[u], x1[u], 0x7632),
+                         __byte_perm(x2[u], x3[u], 0x7632));
+                }
+              } else {
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {           // channels 4 u .. 4 u + 3
+                  const uint32_t a0 = __byte_perm(x0[u], x1[u], 0x5140), a1 = __byte_perm(x0[u], x1[u], 0x7362);
+                  const uint32_t b0 = __byte_perm(x2[u], x3[u], 0x5140), b1 = __byte_perm(x2[u], x3[u], 0x7362);
+                  mma<Q>(acc[h * 16 + 4 * u], ph[kk], pl[kk], ph[kk + 1], pl[kk + 1], e4m3x2_h2(a0 & 0xffff), e4m3x2_h2(b0 & 0xffff));
+                  mma<Q>(acc[h * 16 + 4 * u + 1], ph[kk], pl[kk], ph[kk + 1], pl[kk + 1], e4m3x2_h2(a0 >> 16), e4m3x2_h2(b0 >> 16));
+                  mma<Q>(acc[h * 16 + 4 * u + 2], ph[kk], pl[kk], ph[kk + 1], pl[kk + 1], e4m3x2_h2(a1 & 0xffff), e4m3x2_h2(b1 & 0xffff));
+                  mma<Q>(acc[h * 16 + 4 * u + 3], ph[kk], pl[kk], ph[kk + 1], pl[kk + 1], e4m3x2_h2(a1 >> 16), e4m3x2_h2(b1 >> 16));
+                }
+              }
+            }
+          }
+        __syncwarp();                                   // the stage is free to be written
+      }
+    }
+    cp_wait<0>();
+    l += __shfl_xor_sync(0xffffffffu, l, 1);
+    l += __shfl_xor_sync(0xffffffffu, l, 2);
+    const float back = Q ? ldexpf(1.f, vexp) : 1.f;
+    // column n of channel group c is element c % EPP of the piece c / EPP * 8 + n, and this
+    // lane has columns 2 j4, + 1 of row n8: whole pieces
+    if (t0 == 0 && t1 == nt) {
+      const float inv = l != 0.f ? 1.f / l : 0.f;
+      bf16* o = (bf16*)p.o + (long long)b * p.o_row + (long long)(g * G + h0 + n8) * hd;
+      if (n8 < nh)
+#pragma unroll
+        for (int h = 0; h < VH; ++h)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int ch = (h * 8 + 2 * j4 + e) * EPP;
+            if (ch >= hd) continue;
+            bf16 y[EPP];
+#pragma unroll
+            for (int i = 0; i < EPP; ++i) y[i] = from_f<bf16>((acc[h * EPP + i][e] + acc[h * EPP + i][2 + e]) * inv * back);
+#pragma unroll
+            for (int i = 0; i < EPP; i += 8) {
+              uint32_t w[4];
+#pragma unroll
+              for (int u = 0; u < 4; ++u)
+                w[u] = (uint32_t)__bfloat16_as_ushort(y[i + 2 * u]) | (uint32_t)__bfloat16_as_ushort(y[i + 2 * u + 1]) << 16;
+              if (vec_o) *reinterpret_cast<uint4*>(o + ch + i) = make_uint4(w[0], w[1], w[2], w[3]);
+              else
+#pragma unroll
+                for (int u = 0; u < 8; ++u) o[ch + i + u] = y[i + u];
+            }
+          }
+    } else {
+      const int which = t0 == 0;
+      if (t0 > 0 && t1 == nt) joins = Desc{b, seg, (int)((x - t0) / piece), 0};
+      float* ml = part_ml(p, worker, which);
+      float* po = part_o(p, worker, which) + n8 * hd;
+      if (j4 == 0) {
+        ml[n8 * 2] = m;
+        ml[n8 * 2 + 1] = l;
+      }
+      if (n8 < nh)
+#pragma unroll
+        for (int h = 0; h < VH; ++h)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int ch = (h * 8 + 2 * j4 + e) * EPP;
+            if (ch >= hd) continue;
+#pragma unroll
+            for (int i = 0; i < EPP; i += 4) {
+              float4 y;
+              y.x = (acc[h * EPP + i][e] + acc[h * EPP + i][2 + e]) * back;
+              y.y = (acc[h * EPP + i + 1][e] + acc[h * EPP + i + 1][2 + e]) * back;
+              y.z = (acc[h * EPP + i + 2][e] + acc[h * EPP + i + 2][2 + e]) * back;
+              y.w = (acc[h * EPP + i + 3][e] + acc[h * EPP + i + 3][2 + e]) * back;
+              *reinterpret_cast<float4*>(po + ch + i) = y;
+            }
+          }
+    }
+    x += t1 - t0;
+    at.at += t1 - t0;
+  }
+  if (lane == 0) desc_of(p)[worker] = joins;
+  let_join_start();
+}
+
+// ------------------------------------------------------------------------------------------
+// plain kernel: any width and page size, fp32 or bf16, both storage forms; a worker is a CTA
+// ------------------------------------------------------------------------------------------
+// 32-key tiles of K and V widened to fp32 in shared memory.  Scores: a lane per key, each warp
+// a quarter of the channels for all heads, so a K element serves 8 products; values: a thread
+// per channel, so a V element serves 8.  Bound by shared-memory loads (3 per 8 products).
+namespace {
+constexpr int TK = 32;
+struct PlainSm {
+  long long* slot;   // [TK] slot of each key, -1: takes no part
+  float* q;          // [hd][GT]
+  float* k;          // [TK][ld]
+  float* v;          // [TK][ld]
+  float* part;       // [WARPS][GT][TK]
+  float* w;          // [TK][GT]
+  float* corr;       // [GT]
+  int ld;
+  __host__ __device__ static int stride(int hd) { return (hd + 3) / 4 * 4 + 4; }   // 4 mod 32 words: no conflicts
+  __host__ __device__ static size_t bytes(int hd) {
+    return TK * 8 + sizeof(float) * ((size_t)GT * ((hd + 3) / 4 * 4) + 2 * (size_t)TK * stride(hd) + WARPS * GT * TK + TK * GT + GT);
+  }
+};
 }  // namespace
 
 template <typename T, bool Q>
-__global__ void __launch_bounds__(128) k_paged_attn_any(PagedAttnParams p) {
-  extern __shared__ __align__(16) unsigned char smem[];
-  const int hd = p.c.hd, Hkv = p.c.Hkv, G = p.H / Hkv, ldk = hd + 1;
-  long long* off = reinterpret_cast<long long*>(smem);          // [TK] slot of each key (-1: masked)
-  float* qs = reinterpret_cast<float*>(off + TK);               // [GT][hd]
-  float* Ks = qs + GT * hd;                                     // [TK][hd + 1]
-  float* Vs = Ks + TK * ldk;
-  float* ps = Vs + TK * ldk;                                    // [GT][TK]
-  float* corr = ps + GT * TK;                                   // [GT]
-  const int split = blockIdx.x, n_split = gridDim.x, n_ht = (G + GT - 1) / GT;
-  const int g = blockIdx.y / n_ht, h0 = (blockIdx.y % n_ht) * GT, nh = min(GT, G - h0), b = blockIdx.z;
+__global__ void __launch_bounds__(128) k_paged_attn_simt(PagedAttnParams p, int least, int vec) {
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ long long red[WARPS];
+  const int hd = p.c.hd, hd4 = (hd + 3) / 4 * 4, Hkv = p.c.Hkv, G = p.H / Hkv, n_ht = (G + GT - 1) / GT, segs = Hkv * n_ht;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int len = visible_keys(p.c, p.lens, b, p.len_add, p.st, 221);
-  const int chunk = ((len + n_split - 1) / n_split + TK - 1) / TK * TK;
-  const long long j0 = (long long)split * chunk;
-  const int j1 = (int)min((long long)len, j0 + chunk);
-  const float sl2 = p.scale * 1.4426950408889634f;
-  for (int i = tid; i < nh * hd; i += 128)
-    qs[i] = to_f(((const T*)p.q)[(long long)b * p.q_row + (long long)(g * G + h0) * hd + i]) * sl2;
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};       // heads warp and warp + 4
-  float acc[GT][2];                                             // channels tid and tid + 128
-#pragma unroll
-  for (int h = 0; h < GT; ++h) acc[h][0] = acc[h][1] = 0.f;
-  for (long long j = j0; j < j1; j += TK) {
-    const int nk = (int)min((long long)TK, j1 - j);
-    __syncthreads();
-    if (tid < TK) {
-      long long o = -1;
-      if (tid < nk) {
-        const int page = page_of(p.c, b, (int)j + tid, p.st, 222);
-        if (page >= 0) o = ((long long)page * Hkv + g) * p.c.page_size + ((int)j + tid) % p.c.page_size;
-      }
-      off[tid] = o;
+  PlainSm sm;
+  sm.ld = PlainSm::stride(hd);
+  sm.slot = reinterpret_cast<long long*>(smem);
+  sm.q = reinterpret_cast<float*>(sm.slot + TK);
+  sm.k = sm.q + GT * hd4;
+  sm.v = sm.k + TK * sm.ld;
+  sm.part = sm.v + TK * sm.ld;
+  sm.w = sm.part + WARPS * GT * TK;
+  sm.corr = sm.w + TK * GT;
+  zero_rows(p, TK, (int)sizeof(T));
+  const long long length = line_length(p, segs, TK, red);
+  const long long piece = piece_of(length, gridDim.x, least);
+  const long long w0 = blockIdx.x * piece, w1 = w0 + piece < length ? w0 + piece : length;
+  // channels past the width (up to a multiple of 4) are zeros in q and K
+  for (int i = tid; i < GT * hd4; i += 128) sm.q[i] = 0.f;
+  for (int i = tid; i < TK * sm.ld; i += 128) sm.k[i] = sm.v[i] = 0.f;
+  Desc joins{-1, 0, 0, 0};
+  Place at = w0 < w1 ? line_find(p, segs, TK, w0) : Place{0, 0};
+  for (long long x = w0; x < w1;) {
+    const int b = at.b, len = visible_keys(p.c, p.lens, b, p.len_add, nullptr, 0), nt = (len + TK - 1) / TK;
+    if (at.at >= (long long)nt * segs) {
+      at = Place{b + 1, 0};
+      continue;
     }
+    const int seg = (int)(at.at / nt), t0 = (int)(at.at % nt);
+    const int t1 = nt - t0 < w1 - x ? nt : t0 + (int)(w1 - x);
+    const int g = seg / n_ht, h0 = seg % n_ht * GT, nh = min(GT, G - h0);
+    const float sl2 = p.scale * LOG2E;
     __syncthreads();
-    for (int i = tid; i < TK * hd; i += 128) {
-      const int r = i / hd, d = i - r * hd;
-      const long long o = off[r];
-      float kx = 0.f, vx = 0.f;                                 // masked rows hold zeros: 0 * v is 0 whatever the slot holds
-      if (o >= 0) {
-        if (Q) {
-          kx = e4m3_f(((const uint8_t*)p.c.k)[o * hd + d]) * exp_byte_scale(p.c.ke[o]);
-          vx = e4m3_f(((const uint8_t*)p.c.v)[o * hd + d]) * exp_byte_scale(p.c.ve[o]);
-        } else {
-          kx = to_f(((const T*)p.c.k)[o * hd + d]);
-          vx = to_f(((const T*)p.c.v)[o * hd + d]);
+    for (int i = tid; i < nh * hd; i += 128) {
+      const int h = i / hd, d = i - h * hd;
+      sm.q[d * GT + h] = to_f(((const T*)p.q)[(long long)b * p.q_row + (long long)(g * G + h0) * hd + i]) * sl2;
+    }
+    if (nh < GT)
+      for (int i = tid; i < (GT - nh) * hd; i += 128) sm.q[i / (GT - nh) * GT + nh + i % (GT - nh)] = 0.f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};       // heads warp and warp + 4
+    float acc[GT][2];                                             // channels tid and tid + 128
+#pragma unroll
+    for (int h = 0; h < GT; ++h) acc[h][0] = acc[h][1] = 0.f;
+    for (int t = t0; t < t1; ++t) {
+      __syncthreads();
+      if (tid < TK) {
+        const int key = t * TK + tid;
+        long long s = -1;
+        if (key < len) {
+          const int page = page_of(p.c, b, key, p.st, 222);
+          if (page >= 0) s = ((long long)page * Hkv + g) * p.c.page_size + key % p.c.page_size;
+        }
+        sm.slot[tid] = s;
+      }
+      __syncthreads();
+      // masked rows hold zeros: 0 * v is 0 whatever the slot holds
+      if (vec) {
+        const int q4 = hd / 4;
+        for (int i = tid; i < TK * q4; i += 128) {
+          const int r = i / q4, c = i - r * q4;
+          const long long s = sm.slot[r];
+          float4 kx = make_float4(0.f, 0.f, 0.f, 0.f), vx = kx;
+          if (s >= 0) {
+            if (Q) {
+              const uint32_t kw = __ldg((const uint32_t*)p.c.k + s * q4 + c), vw = __ldg((const uint32_t*)p.c.v + s * q4 + c);
+              const float ks = exp_byte_scale(p.c.ke[s]), vs = exp_byte_scale(p.c.ve[s]);
+              kx = make_float4(e4m3_f(kw & 255) * ks, e4m3_f(kw >> 8 & 255) * ks, e4m3_f(kw >> 16 & 255) * ks, e4m3_f(kw >> 24) * ks);
+              vx = make_float4(e4m3_f(vw & 255) * vs, e4m3_f(vw >> 8 & 255) * vs, e4m3_f(vw >> 16 & 255) * vs, e4m3_f(vw >> 24) * vs);
+            } else if (sizeof(T) == 4) {
+              kx = __ldg((const float4*)p.c.k + s * q4 + c);
+              vx = __ldg((const float4*)p.c.v + s * q4 + c);
+            } else {
+              const uint2 kw = __ldg((const uint2*)p.c.k + s * q4 + c), vw = __ldg((const uint2*)p.c.v + s * q4 + c);
+              kx = make_float4(__uint_as_float(kw.x << 16), __uint_as_float(kw.x & 0xffff0000u), __uint_as_float(kw.y << 16),
+                               __uint_as_float(kw.y & 0xffff0000u));
+              vx = make_float4(__uint_as_float(vw.x << 16), __uint_as_float(vw.x & 0xffff0000u), __uint_as_float(vw.y << 16),
+                               __uint_as_float(vw.y & 0xffff0000u));
+            }
+          }
+          *reinterpret_cast<float4*>(sm.k + r * sm.ld + 4 * c) = kx;
+          *reinterpret_cast<float4*>(sm.v + r * sm.ld + 4 * c) = vx;
+        }
+      } else {
+        for (int i = tid; i < TK * hd; i += 128) {
+          const int r = i / hd, d = i - r * hd;
+          const long long s = sm.slot[r];
+          float kx = 0.f, vx = 0.f;
+          if (s >= 0) {
+            if (Q) {
+              kx = e4m3_f(((const uint8_t*)p.c.k)[s * hd + d]) * exp_byte_scale(p.c.ke[s]);
+              vx = e4m3_f(((const uint8_t*)p.c.v)[s * hd + d]) * exp_byte_scale(p.c.ve[s]);
+            } else {
+              kx = to_f(((const T*)p.c.k)[s * hd + d]);
+              vx = to_f(((const T*)p.c.v)[s * hd + d]);
+            }
+          }
+          sm.k[r * sm.ld + d] = kx;
+          sm.v[r * sm.ld + d] = vx;
         }
       }
-      Ks[r * ldk + d] = kx;
-      Vs[r * ldk + d] = vx;
-    }
-    __syncthreads();
+      __syncthreads();
+      {
+        const int n4 = hd4 / 4, c0 = n4 * warp / WARPS, c1 = n4 * (warp + 1) / WARPS;
+        float s[GT] = {};
+        for (int c = c0; c < c1; ++c) {
+          const float4 k4 = *reinterpret_cast<const float4*>(sm.k + lane * sm.ld + 4 * c);
+          const float kk[4] = {k4.x, k4.y, k4.z, k4.w};
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int h = warp + 4 * u;
-      if (h < nh) {
+          for (int e = 0; e < 4; ++e) {
+            const float4 qa = *reinterpret_cast<const float4*>(sm.q + (4 * c + e) * GT);
+            const float4 qb = *reinterpret_cast<const float4*>(sm.q + (4 * c + e) * GT + 4);
+            s[0] = fmaf(qa.x, kk[e], s[0]); s[1] = fmaf(qa.y, kk[e], s[1]);
+            s[2] = fmaf(qa.z, kk[e], s[2]); s[3] = fmaf(qa.w, kk[e], s[3]);
+            s[4] = fmaf(qb.x, kk[e], s[4]); s[5] = fmaf(qb.y, kk[e], s[5]);
+            s[6] = fmaf(qb.z, kk[e], s[6]); s[7] = fmaf(qb.w, kk[e], s[7]);
+          }
+        }
+#pragma unroll
+        for (int h = 0; h < GT; ++h) sm.part[(warp * GT + h) * TK + lane] = s[h];
+      }
+      __syncthreads();
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int h = warp + 4 * u;
         float s = 0.f;
-        for (int d = 0; d < hd; ++d) s = fmaf(qs[h * hd + d], Ks[lane * ldk + d], s);
-        if (off[lane] < 0) s = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) s += sm.part[(w * GT + h) * TK + lane];
+        if (sm.slot[lane] < 0) s = -INFINITY;
         const float mx = fmaxf(m[u], warp_max(s));
         const float base = mx == -INFINITY ? 0.f : mx;
         const float e = exp2f(s - base), c = exp2f(m[u] - base);
         m[u] = mx;
         l[u] = l[u] * c + warp_sum(e);
-        ps[h * TK + lane] = e;
-        if (lane == 0) corr[h] = c;
+        sm.w[lane * GT + h] = e;
+        if (lane == 0) sm.corr[h] = c;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int d = tid + 128 * u;
+        if (d < hd) {
+#pragma unroll
+          for (int h = 0; h < GT; ++h) acc[h][u] *= sm.corr[h];
+#pragma unroll 8
+          for (int r = 0; r < TK; ++r) {
+            const float v = sm.v[r * sm.ld + d];
+            const float4 wa = *reinterpret_cast<const float4*>(sm.w + r * GT), wb = *reinterpret_cast<const float4*>(sm.w + r * GT + 4);
+            acc[0][u] = fmaf(wa.x, v, acc[0][u]); acc[1][u] = fmaf(wa.y, v, acc[1][u]);
+            acc[2][u] = fmaf(wa.z, v, acc[2][u]); acc[3][u] = fmaf(wa.w, v, acc[3][u]);
+            acc[4][u] = fmaf(wb.x, v, acc[4][u]); acc[5][u] = fmaf(wb.y, v, acc[5][u]);
+            acc[6][u] = fmaf(wb.z, v, acc[6][u]); acc[7][u] = fmaf(wb.w, v, acc[7][u]);
+          }
+        }
+      }
+    }
+    const bool whole = t0 == 0 && t1 == nt;
+    const int which = t0 == 0;
+    if (t0 > 0 && t1 == nt) joins = Desc{b, seg, (int)((x - t0) / piece), 0};
+    __syncthreads();
+    if (lane == 0) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int h = warp + 4 * u;
+        sm.corr[h] = l[u];
+        if (!whole) {
+          float* ml = part_ml(p, blockIdx.x, which);
+          ml[h * 2] = m[u];
+          ml[h * 2 + 1] = l[u];
+        }
       }
     }
     __syncthreads();
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const int d = tid + 128 * u;
-      if (d < hd) {
+      if (d >= hd) continue;
 #pragma unroll
-        for (int h = 0; h < GT; ++h)
-          if (h < nh) acc[h][u] *= corr[h];
-        for (int r = 0; r < TK; ++r) {
-          const float v = Vs[r * ldk + d];
-#pragma unroll
-          for (int h = 0; h < GT; ++h)
-            if (h < nh) acc[h][u] = fmaf(ps[h * TK + r], v, acc[h][u]);
-        }
+      for (int h = 0; h < GT; ++h) {
+        if (h >= nh) continue;
+        if (whole)
+          ((T*)p.o)[(long long)b * p.o_row + (long long)(g * G + h0 + h) * hd + d] =
+              from_f<T>(sm.corr[h] != 0.f ? acc[h][u] / sm.corr[h] : 0.f);
+        else
+          part_o(p, blockIdx.x, which)[h * hd + d] = acc[h][u];
       }
     }
+    x += t1 - t0;
+    at.at += t1 - t0;
   }
-  // joined here (one range) or by k_paged_attn_join
-  __syncthreads();
-#pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const int h = warp + 4 * u;
-    if (h < nh && lane == 0) {
-      if (n_split == 1) {
-        corr[h] = l[u];
-      } else {
-        const long long s = ((long long)b * p.H + g * G + h0 + h) * n_split + split;
-        p.part_ml[2 * s] = m[u];
-        p.part_ml[2 * s + 1] = l[u];
-      }
-    }
-  }
-  __syncthreads();
-#pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const int d = tid + 128 * u;
-    if (d >= hd) continue;
-#pragma unroll
-    for (int h = 0; h < GT; ++h) {
-      if (h >= nh) continue;
-      const int head = g * G + h0 + h;
-      if (n_split == 1) {
-        ((T*)p.o)[(long long)b * p.o_row + (long long)head * hd + d] = from_f<T>(corr[h] != 0.f ? acc[h][u] / corr[h] : 0.f);
-      } else {
-        p.part_o[(((long long)b * p.H + head) * n_split + split) * hd + d] = acc[h][u];
-      }
-    }
-  }
+  if (tid == 0) desc_of(p)[blockIdx.x] = joins;
+  let_join_start();
 }
 
+// ------------------------------------------------------------------------------------------
+// join: CTA i joins the parts of the group that worker i finished
+// ------------------------------------------------------------------------------------------
+// 512 threads: 4 slices of the parts, 128 channels each; weights in shared memory.
+constexpr int JT = 512;
 template <typename T>
-__global__ void __launch_bounds__(128) k_paged_attn_join(PagedAttnParams p, int n_split) {
-  const long long bh = blockIdx.x;
-  const int b = (int)(bh / p.H), h = (int)(bh % p.H), hd = p.c.hd;
-  const float* ml = p.part_ml + bh * n_split * 2;
-  float M = -INFINITY;
-  for (int s = 0; s < n_split; ++s) M = fmaxf(M, ml[2 * s]);
-  const float base = M == -INFINITY ? 0.f : M;
-  float L = 0.f;
-  for (int s = 0; s < n_split; ++s) L += exp2f(ml[2 * s] - base) * ml[2 * s + 1];
-  for (int d = threadIdx.x; d < hd; d += 128) {
-    float o = 0.f;
-    for (int s = 0; s < n_split; ++s) o += exp2f(ml[2 * s] - base) * p.part_o[(bh * n_split + s) * hd + d];
-    ((T*)p.o)[(long long)b * p.o_row + (long long)h * hd + d] = from_f<T>(L != 0.f ? o / L : 0.f);
+__global__ void __launch_bounds__(JT) k_paged_attn_join(PagedAttnParams p) {
+  extern __shared__ float wj[];                       // [parts] 2^(m - M) of one head
+  __shared__ float red[JT / 32], sum[JT / 128][128];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Desc d = desc_of(p)[blockIdx.x];
+  if (d.b < 0) return;
+  const int hd = p.c.hd, G = p.H / p.c.Hkv, n_ht = (G + GT - 1) / GT;
+  const int g = d.seg / n_ht, h0 = d.seg % n_ht * GT, nh = min(GT, G - h0), n = (int)blockIdx.x - d.first + 1;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, slice = tid >> 7, c = tid & 127;
+  // part 1 of the first worker, part 0 of the others
+  for (int h = 0; h < nh; ++h) {
+    float M = -INFINITY, L = 0.f;
+    for (int s = tid; s < n; s += JT) M = fmaxf(M, part_ml(p, d.first + s, s == 0)[h * 2]);
+    M = warp_max(M);
+    __syncthreads();
+    if (lane == 0) red[warp] = M;
+    __syncthreads();
+    M = warp_max(lane < JT / 32 ? red[lane] : -INFINITY);
+    const float base = M == -INFINITY ? 0.f : M;
+    for (int s = tid; s < n; s += JT) {
+      const float* ml = part_ml(p, d.first + s, s == 0);
+      const float w = exp2f(ml[h * 2] - base);
+      wj[s] = w;
+      L += w * ml[h * 2 + 1];
+    }
+    L = block_sum(L, red);                            // (its barriers also cover wj)
+    for (int ch0 = 0; ch0 < hd; ch0 += 128) {
+      const int ch = ch0 + c;
+      float o = 0.f;
+      if (ch < hd) {
+#pragma unroll 8
+        for (int s = slice; s < n; s += JT / 128) o = fmaf(wj[s], part_o(p, d.first + s, s == 0)[h * hd + ch], o);
+      }
+      sum[slice][c] = o;
+      __syncthreads();
+      if (slice == 0 && ch < hd) {
+        o = (sum[0][c] + sum[1][c]) + (sum[2][c] + sum[3][c]);
+        ((T*)p.o)[(long long)d.b * p.o_row + (long long)(g * G + h0 + h) * hd + ch] = from_f<T>(L != 0.f ? o / L : 0.f);
+      }
+      __syncthreads();
+    }
   }
 }
 
-// Ranges per sequence: enough CTAs for four on each SM, at most one per 128 positions the
-// table can hold.
-static int any_splits(const PagedView& c, int B, int H) {
-  const long long ctas = (long long)B * c.Hkv * ((H / c.Hkv + GT - 1) / GT);
-  const long long cap = (long long)c.max_pages * c.page_size;
-  const long long want = (4LL * device_sm_count() + ctas - 1) / ctas;
-  return (int)std::max<long long>(1, std::min<long long>(std::min<long long>(want, (cap + 127) / 128), 1024));
+// ------------------------------------------------------------------------------------------
+// launch
+// ------------------------------------------------------------------------------------------
+namespace {
+// 16-byte copies need rows and bases on 16 bytes
+bool mma_takes(int dtype, const PagedView& c) {
+  const int rb = c.hd * (c.e4m3 ? 1 : 2);
+  return dtype == 1 && c.hd % 8 == 0 && rb % 16 == 0 && !(((uintptr_t)c.k | (uintptr_t)c.v) & 15);
 }
+int workers_mma() { return device_sm_count() * 2 * WARPS; }
+int workers_simt() { return device_sm_count() * 4; }
+size_t scratch_bytes(int workers, int hd) { return (size_t)workers * (sizeof(Desc) + 2 * GT * (hd + 2) * sizeof(float)); }
 
-size_t paged_attn_scratch(int dtype, const PagedView& c, int B, int H) {
-  (void)dtype;
-  const int n = any_splits(c, B, H);
-  return n > 1 ? (size_t)B * H * n * (c.hd + 2) * sizeof(float) : 0;
+template <typename T> int launch_join(const PagedAttnParams& p, int workers, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)workers);
+  cfg.blockDim = dim3(JT);
+  cfg.dynamicSmemBytes = (size_t)workers * sizeof(float);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // launched while the workers finish
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, k_paged_attn_join<T>, p) != cudaSuccess) return -1;
+  note_launch();
+  return 0;
+}
+}  // namespace
+
+// The same for every batch and head count: the parts belong to the workers.
+size_t paged_attn_scratch(const PagedView& c) {
+  return std::max(scratch_bytes(workers_mma(), c.hd), scratch_bytes(workers_simt(), c.hd));
 }
 
 int launch_paged_attn(int dtype, const PagedAttnParams& p0, cudaStream_t s) {
   PagedAttnParams p = p0;
-  const int G = p.H / p.c.Hkv, n_ht = (G + GT - 1) / GT, n_split = any_splits(p.c, p.B, p.H);
-  p.part_o = (float*)p.scratch;
-  p.part_ml = p.part_o + (size_t)p.B * p.H * n_split * p.c.hd;
-  const dim3 grid((unsigned)n_split, (unsigned)(p.c.Hkv * n_ht), (unsigned)p.B);
-  const int smem = (int)any_smem(p.c.hd), most = (int)any_smem(256);
-#define RDT_ANY(TT, QQ)                                                                     \
-  do {                                                                                      \
-    if (!ensure_smem_limit((const void*)k_paged_attn_any<TT, QQ>, most)) return -1;         \
-    k_paged_attn_any<TT, QQ><<<grid, 128, smem, s>>>(p);                                    \
-    note_launch();                                                                          \
-    if (n_split > 1) {                                                                      \
-      k_paged_attn_join<TT><<<(unsigned)(p.B * p.H), 128, 0, s>>>(p, n_split);              \
-      note_launch();                                                                        \
-    }                                                                                       \
-  } while (0)
-  if (dtype == 0) {
-    if (p.c.e4m3) RDT_ANY(float, true);
-    else RDT_ANY(float, false);
-  } else {
-    if (p.c.e4m3) RDT_ANY(bf16, true);
-    else RDT_ANY(bf16, false);
+  const bool tc = mma_takes(dtype, p.c);
+  const int workers = tc ? workers_mma() : workers_simt();
+  p.part_ml = reinterpret_cast<float*>((char*)p.scratch + (size_t)workers * sizeof(Desc));
+  p.part_o = p.part_ml + (size_t)workers * 2 * GT * 2;
+  if (tc) {
+#define RDT_MMA(HD, QQ)                                                                                            do {                                                                                                               constexpr int smem = WARPS * Ring<HD, QQ>::BYTES;                                                                if (!ensure_smem_limit((const void*)k_paged_attn_mma<HD, QQ>, smem)) return -1;                                  k_paged_attn_mma<HD, QQ><<<workers / WARPS, 32 * WARPS, smem, s>>>(p, 2);                                      } while (0)
+    if (p.c.e4m3) {
+      if (p.c.hd <= 64) RDT_MMA(64, true);
+      else if (p.c.hd <= 128) RDT_MMA(128, true);
+      else RDT_MMA(256, true);
+    } else {
+      if (p.c.hd <= 64) RDT_MMA(64, false);
+      else if (p.c.hd <= 128) RDT_MMA(128, false);
+      else RDT_MMA(256, false);
+    }
+#undef RDT_MMA
+    note_launch();
+    return launch_join<bf16>(p, workers, s);
   }
-#undef RDT_ANY
-  return 0;
+  const int smem = (int)PlainSm::bytes(p.c.hd), most = (int)PlainSm::bytes(256);
+  const int eb = p.c.e4m3 ? 1 : dtype == 0 ? 4 : 2;
+  const int vec = p.c.hd % 4 == 0 && !(((uintptr_t)p.c.k | (uintptr_t)p.c.v) & (4 * eb - 1));
+#define RDT_SIMT(TT, QQ)                                                                      do {                                                                                          if (!ensure_smem_limit((const void*)k_paged_attn_simt<TT, QQ>, most)) return -1;            k_paged_attn_simt<TT, QQ><<<workers, 128, smem, s>>>(p, 2, vec);                          } while (0)
+  if (dtype == 0) {
+    if (p.c.e4m3) RDT_SIMT(float, true);
+    else RDT_SIMT(float, false);
+  } else {
+    if (p.c.e4m3) RDT_SIMT(bf16, true);
+    else RDT_SIMT(bf16, false);
+  }
+#undef RDT_SIMT
+  note_launch();
+  return dtype == 0 ? launch_join<float>(p, workers, s) : launch_join<bf16>(p, workers, s);
 }
 
 }  // namespace rdt

@@ -286,7 +286,7 @@ struct PagedAttnParams {
 };
 void launch_paged_write(int dtype, const PagedWriteParams& p, cudaStream_t s);
 void launch_paged_read(int dtype, const PagedReadParams& p, cudaStream_t s);
-size_t paged_attn_scratch(int dtype, const PagedView& c, int B, int H);
+size_t paged_attn_scratch(const PagedView& c);
 int launch_paged_attn(int dtype, const PagedAttnParams& p, cudaStream_t s);   // returns 0 on success
 
 struct SampleParams {

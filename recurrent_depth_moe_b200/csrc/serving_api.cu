@@ -84,7 +84,7 @@ size_t rdt_paged_attention_workspace_size(const rdt_paged_cache* cache, int batc
   if (check_paged_cache(cache) != RDT_OK || batch <= 0 || batch > cache->batch || n_heads <= 0 ||
       n_heads % cache->n_kv_heads)
     return 0;
-  return 256 + (paged_attn_scratch(cache->dtype, paged_view(cache, 0), batch, n_heads) + 255) / 256 * 256;
+  return 256 + (paged_attn_scratch(paged_view(cache, 0)) + 255) / 256 * 256;
 }
 
 rdt_status rdt_paged_attention(const rdt_paged_cache* cache, int loop, const void* q, long long q_ld,

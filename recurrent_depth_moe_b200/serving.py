@@ -187,7 +187,8 @@ def paged_kv_read(lens: torch.Tensor, cache: PagedKVCache, t_out: Optional[int] 
 def paged_attention_workspace(cache: PagedKVCache, n_heads: int, batch: Optional[int] = None) -> torch.Tensor:
     """Workspace of paged_attention calls with up to `batch` sequences (the table's rows without
     it), for one call at a time."""
-    need = int(N.load().rdt_paged_attention_workspace_size(cache._ref, cache.batch if batch is None else batch, n_heads))
+    with torch.cuda.device(cache.device):
+        need = int(_lib().rdt_paged_attention_workspace_size(cache._ref, cache.batch if batch is None else batch, n_heads))
     if need == 0:
         raise N.RdtError("rdt_paged_attention_workspace_size", N.RDT_ERR_INVALID_ARG)
     return torch.empty(need, dtype=torch.uint8, device=cache.device)
