@@ -25,20 +25,30 @@ def _lib():
     return N.load()
 
 
+_fns: dict = {}
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else \
+    lambda i: torch.cuda.current_stream(i).cuda_stream
+
+
 def _call(name: str, device: torch.device, *args):
-    """The entry point on the device's current stream, with that device current."""
-    fn = getattr(_lib(), name)
-    if device.index == torch.cuda.current_device():
-        rc = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    """The entry point on the device's current stream, with that device current.  (A serving step
+    makes these calls every few microseconds: the entry point is looked up once.)"""
+    fn = _fns.get(name)
+    if fn is None:
+        fn = _fns[name] = getattr(_lib(), name)
+    i = device.index
+    if i == _current_device():
+        rc = fn(*args, _raw_stream(i))
     else:
         with torch.cuda.device(device):
-            rc = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+            rc = fn(*args, _raw_stream(i))
     if rc != N.RDT_OK:
         raise N.RdtError(name, rc)
 
 
 def _check(t, name: str, dtype, shape, device=None):
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dtype or tuple(t.shape) != tuple(shape) or \
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dtype or t.shape != shape or \
             not t.is_contiguous() or (device is not None and t.device != device):
         got = f"{t.device} {t.dtype} {tuple(t.shape)} contiguous={t.is_contiguous()}" if isinstance(t, torch.Tensor) \
             else type(t).__name__
@@ -47,14 +57,17 @@ def _check(t, name: str, dtype, shape, device=None):
 
 def _check_rows(t, name: str, dtype, shape, device):
     """A [rows, heads, hd] tensor whose rows are contiguous; the rows may be spaced apart."""
-    if not isinstance(t, torch.Tensor) or t.device != device or t.dtype != dtype or tuple(t.shape) != tuple(shape):
+    if not isinstance(t, torch.Tensor) or t.device != device or t.dtype != dtype or t.shape != shape:
         got = f"{t.device} {t.dtype} {tuple(t.shape)}" if isinstance(t, torch.Tensor) else type(t).__name__
         raise ValueError(f"{name}: expected {device} {dtype} {tuple(shape)}, got {got}")
-    w = shape[1] * shape[2]
-    if (shape[2] > 1 and t.stride(2) != 1) or (shape[1] > 1 and t.stride(1) != shape[2]) or \
-            (shape[0] > 1 and t.stride(0) < w):
-        raise ValueError(f"{name}: each row must be contiguous and the rows must not overlap, got strides {t.stride()}")
-    return t.stride(0) if shape[0] > 1 else w
+    rows, heads, hd = shape
+    w = heads * hd
+    if t.is_contiguous():
+        return w
+    st = t.stride()
+    if (hd > 1 and st[2] != 1) or (heads > 1 and st[1] != hd) or (rows > 1 and st[0] < w):
+        raise ValueError(f"{name}: each row must be contiguous and the rows must not overlap, got strides {st}")
+    return st[0] if rows > 1 else w
 
 
 class PagedKVCache:
@@ -105,6 +118,7 @@ class PagedKVCache:
         self._struct = s
         self._ref = ctypes.byref(s)
         self.status = torch.zeros(4, dtype=torch.int32, device=dev)
+        self._status = self.status.data_ptr()
 
     k = property(lambda self: self._k)
     v = property(lambda self: self._v)
@@ -160,7 +174,7 @@ def paged_kv_write(k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor, ca
         raise ValueError("k and v must have the same row stride")
     _check(positions, "positions", torch.int32, (n,), c.device)
     _call("rdt_paged_kv_write", c.device, c._ref, loop, k.data_ptr(), v.data_ptr(), ld, positions.data_ptr(), n, seq,
-          c.status.data_ptr())
+          c._status)
 
 
 def paged_kv_read(lens: torch.Tensor, cache: PagedKVCache, t_out: Optional[int] = None, loop: int = 0,
@@ -180,7 +194,7 @@ def paged_kv_read(lens: torch.Tensor, cache: PagedKVCache, t_out: Optional[int] 
         for o, name in zip(out, ("out[0]", "out[1]")):
             _check(o, name, c.torch_dtype, (B, c.n_kv_heads, t_out, c.head_dim), c.device)
     _call("rdt_paged_kv_read", c.device, c._ref, loop, lens.data_ptr(), B, t_out, out[0].data_ptr(),
-          out[1].data_ptr(), c.status.data_ptr())
+          out[1].data_ptr(), c._status)
     return out
 
 
@@ -216,7 +230,7 @@ def paged_attention(q: torch.Tensor, lens: torch.Tensor, cache: PagedKVCache, lo
         raise ValueError(f"workspace: expected a contiguous tensor on {c.device}")
     _call("rdt_paged_attention", c.device, c._ref, loop, q.data_ptr(), q_ld, lens.data_ptr(), B, H,
           1.0 / math.sqrt(c.head_dim) if scale is None else float(scale), out.data_ptr(), o_ld, workspace.data_ptr(),
-          workspace.numel() * workspace.element_size(), c.status.data_ptr())
+          workspace.numel() * workspace.element_size(), c._status)
     return out
 
 
