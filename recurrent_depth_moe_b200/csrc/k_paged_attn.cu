@@ -44,13 +44,21 @@ __device__ __forceinline__ float ex2(float x) {
 // the line of work
 // ------------------------------------------------------------------------------------------
 // Units per sequence: ceil(keys / tile) tiles for each of `segs` (kv head, head group) pairs.
-__device__ __forceinline__ int tiles_of(const PagedAttnParams& p, int b, int tile) {
-  return (visible_keys(p.c, p.lens, b, p.len_add, p.st, 221) + tile - 1) / tile;
-}
-// Length of the line (all 128 threads of the CTA; red: 4 words of shared memory).
-__device__ long long line_length(const PagedAttnParams& p, int segs, int tile, long long* red) {
+constexpr int LENS = 512;           // lengths kept in shared memory (of a longer batch: none)
+struct Lens {
+  const PagedAttnParams& p;
+  const int* kept;                  // shared memory, or null
+  __device__ __forceinline__ int keys(int b) const { return kept ? kept[b] : visible_keys(p.c, p.lens, b, p.len_add, nullptr, 0); }
+  __device__ __forceinline__ int tiles(int b, int tile) const { return (keys(b) + tile - 1) / tile; }
+};
+// Length of the line (all 128 threads of the CTA; keep: LENS ints, red: 4 words of shared memory).
+__device__ long long line_length(const PagedAttnParams& p, int segs, int tile, int* keep, long long* red) {
   long long n = 0;
-  for (int b = threadIdx.x; b < p.B; b += 128) n += (long long)tiles_of(p, b, tile) * segs;
+  for (int b = threadIdx.x; b < p.B; b += 128) {
+    const int len = visible_keys(p.c, p.lens, b, p.len_add, p.st, 221);
+    if (p.B <= LENS) keep[b] = len;
+    n += (long long)((len + tile - 1) / tile) * segs;
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = n;
@@ -62,12 +70,12 @@ struct Place {
   int b;
   long long at;
 };
-__device__ __forceinline__ Place line_find(const PagedAttnParams& p, int segs, int tile, long long x) {
+__device__ __forceinline__ Place line_find(const Lens& lens, int segs, int tile, long long x) {
   const int lane = threadIdx.x & 31;
   long long base = 0;
-  for (int b0 = 0; b0 < p.B; b0 += 32) {
+  for (int b0 = 0; b0 < lens.p.B; b0 += 32) {
     const int b = b0 + lane;
-    const long long n = b < p.B ? (long long)tiles_of(p, b, tile) * segs : 0;
+    const long long n = b < lens.p.B ? (long long)lens.tiles(b, tile) * segs : 0;
     long long c = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -81,7 +89,7 @@ __device__ __forceinline__ Place line_find(const PagedAttnParams& p, int segs, i
     }
     base += __shfl_sync(0xffffffffu, c, 31);
   }
-  return Place{p.B, 0};
+  return Place{lens.p.B, 0};
 }
 // Units of a worker: an equal share, but no less than `least` (a short line is not spread thin).
 __device__ __forceinline__ long long piece_of(long long length, int workers, int least) {
@@ -105,10 +113,10 @@ __device__ __forceinline__ float* part_o(const PagedAttnParams& p, int worker, i
   return p.part_o + ((long long)worker * 2 + which) * GT * p.c.hd;
 }
 __device__ __forceinline__ Desc* desc_of(const PagedAttnParams& p) { return reinterpret_cast<Desc*>(p.scratch); }
-__device__ __forceinline__ void zero_rows(const PagedAttnParams& p, int tile, int es) {
+__device__ __forceinline__ void zero_rows(const PagedAttnParams& p, const Lens& lens, int es) {
   const int n = p.H * p.c.hd * es / 2;   // 16-bit words of a row
   for (int b = blockIdx.x; b < p.B; b += gridDim.x)
-    if (tiles_of(p, b, tile) == 0)
+    if (lens.keys(b) == 0)
       for (int i = threadIdx.x; i < n; i += 128) ((uint16_t*)p.o)[(long long)b * p.o_row * es / 2 + i] = 0;
 }
 __device__ __forceinline__ void let_join_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
@@ -195,12 +203,14 @@ __global__ void __launch_bounds__(32 * WARPS, HD <= 128 ? 2 : 1) k_paged_attn_mm
   constexpr int NC = VH * EPP;                        // groups of 8 channels
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ long long red[WARPS];
+  __shared__ int kept[LENS];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, j4 = lane & 3, n8 = lane >> 2;
   const int hd = p.c.hd, Hkv = p.c.Hkv, G = p.H / Hkv, n_ht = (G + GT - 1) / GT, segs = Hkv * n_ht;
   const int ps = p.c.page_size, row_bytes = hd * (Q ? 1 : 2), pieces = row_bytes / 16;
   const bool vec_o = !(((uintptr_t)p.o | (uintptr_t)(p.o_row * 2)) & 15) && hd % 8 == 0;
-  zero_rows(p, KEYS, 2);
-  const long long length = line_length(p, segs, KEYS, red);
+  const long long length = line_length(p, segs, KEYS, kept, red);
+  const Lens lens{p, p.B <= LENS ? kept : nullptr};
+  zero_rows(p, lens, 2);
   const int worker = blockIdx.x * WARPS + warp;
   const long long piece = piece_of(length, gridDim.x * WARPS, least);
   const long long w0 = worker * piece, w1 = w0 + piece < length ? w0 + piece : length;
@@ -211,10 +221,10 @@ __global__ void __launch_bounds__(32 * WARPS, HD <= 128 ? 2 : 1) k_paged_attn_mm
     for (int i = lane; i < Ring<HD, Q>::BYTES / 16; i += 32) reinterpret_cast<uint4*>(ring)[i] = make_uint4(0, 0, 0, 0);
   __syncwarp();
   Desc joins{-1, 0, 0, 0};
-  Place at = w0 < w1 ? line_find(p, segs, KEYS, w0) : Place{0, 0};
+  Place at = w0 < w1 ? line_find(lens, segs, KEYS, w0) : Place{0, 0};
   for (long long x = w0; x < w1;) {
     // ---- one (sequence, head group): tiles t0 .. t1 - 1 of its nt
-    const int b = at.b, len = visible_keys(p.c, p.lens, b, p.len_add, nullptr, 0), nt = (len + KEYS - 1) / KEYS;
+    const int b = at.b, len = lens.keys(b), nt = (len + KEYS - 1) / KEYS;
     if (at.at >= (long long)nt * segs) {
       at = Place{b + 1, 0};
       continue;
@@ -509,6 +519,7 @@ template <typename T, bool Q>
 __global__ void __launch_bounds__(128) k_paged_attn_simt(PagedAttnParams p, int least, int vec) {
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ long long red[WARPS];
+  __shared__ int kept[LENS];
   const int hd = p.c.hd, hd4 = (hd + 3) / 4 * 4, Hkv = p.c.Hkv, G = p.H / Hkv, n_ht = (G + GT - 1) / GT, segs = Hkv * n_ht;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   PlainSm sm;
@@ -520,17 +531,18 @@ __global__ void __launch_bounds__(128) k_paged_attn_simt(PagedAttnParams p, int 
   sm.part = sm.v + TK * sm.ld;
   sm.w = sm.part + WARPS * GT * TK;
   sm.corr = sm.w + TK * GT;
-  zero_rows(p, TK, (int)sizeof(T));
-  const long long length = line_length(p, segs, TK, red);
+  const long long length = line_length(p, segs, TK, kept, red);
+  const Lens lens{p, p.B <= LENS ? kept : nullptr};
+  zero_rows(p, lens, (int)sizeof(T));
   const long long piece = piece_of(length, gridDim.x, least);
   const long long w0 = blockIdx.x * piece, w1 = w0 + piece < length ? w0 + piece : length;
   // channels past the width (up to a multiple of 4) are zeros in q and K
   for (int i = tid; i < GT * hd4; i += 128) sm.q[i] = 0.f;
   for (int i = tid; i < TK * sm.ld; i += 128) sm.k[i] = sm.v[i] = 0.f;
   Desc joins{-1, 0, 0, 0};
-  Place at = w0 < w1 ? line_find(p, segs, TK, w0) : Place{0, 0};
+  Place at = w0 < w1 ? line_find(lens, segs, TK, w0) : Place{0, 0};
   for (long long x = w0; x < w1;) {
-    const int b = at.b, len = visible_keys(p.c, p.lens, b, p.len_add, nullptr, 0), nt = (len + TK - 1) / TK;
+    const int b = at.b, len = lens.keys(b), nt = (len + TK - 1) / TK;
     if (at.at >= (long long)nt * segs) {
       at = Place{b + 1, 0};
       continue;
@@ -809,7 +821,7 @@ int launch_paged_attn(int dtype, const PagedAttnParams& p0, cudaStream_t s) {
   const int smem = (int)PlainSm::bytes(p.c.hd), most = (int)PlainSm::bytes(256);
   const int eb = p.c.e4m3 ? 1 : dtype == 0 ? 4 : 2;
   const int vec = p.c.hd % 4 == 0 && !(((uintptr_t)p.c.k | (uintptr_t)p.c.v) & (4 * eb - 1));
-#define RDT_SIMT(TT, QQ)                                                                      do {                                                                                          if (!ensure_smem_limit((const void*)k_paged_attn_simt<TT, QQ>, most)) return -1;            k_paged_attn_simt<TT, QQ><<<workers, 128, smem, s>>>(p, 2, vec);                          } while (0)
+#define RDT_SIMT(TT, QQ)                                                                      do {                                                                                          if (!ensure_smem_limit((const void*)k_paged_attn_simt<TT, QQ>, most)) return -1;            k_paged_attn_simt<TT, QQ><<<workers, 128, smem, s>>>(p, 1, vec);                          } while (0)
   if (dtype == 0) {
     if (p.c.e4m3) RDT_SIMT(float, true);
     else RDT_SIMT(float, false);

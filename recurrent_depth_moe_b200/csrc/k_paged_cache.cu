@@ -111,10 +111,22 @@ __global__ void __launch_bounds__(NT) k_paged_write_vec(PagedWriteParams p) {
       for (int i = 0; i < RPT; ++i) {
         unpack<T>(w[kv][i], x[i]);
 #pragma unroll
-        for (int e = 0; e < N; ++e) a = fmaxf(a, finite_abs(x[i][e]));
+        for (int e = 0; e < N; ++e) a = fmaxf(a, fabsf(x[i][e]));   // (fmaxf drops NaN)
       }
 #pragma unroll
       for (int o = GL / 2; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(group, a, o));
+      if (a == INFINITY) {                                 // infinities leave the scale alone
+        a = 0.f;
+#pragma unroll
+        for (int i = 0; i < RPT; ++i)
+#pragma unroll
+          for (int e = 0; e < N; ++e) {
+            a = fmaxf(a, finite_abs(x[i][e]));
+            x[i][e] = inf_to_nan(x[i][e]);
+          }
+#pragma unroll
+        for (int o = GL / 2; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(group, a, o));
+      }
       const int E = row_exponent(a);
       const float inv = pow2_neg(E);
       uint8_t* dst = (uint8_t*)(kv ? p.c.v : p.c.k) + slot * hd;

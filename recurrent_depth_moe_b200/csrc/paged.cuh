@@ -33,14 +33,17 @@ __device__ __forceinline__ float finite_abs(float x) {
   const float a = fabsf(x);
   return a <= 3.402823466e38f ? a : 0.f;
 }
-// e4m3 of x * inv, round to nearest even; e4m3 has no infinity, so +-inf is stored as NaN (as
-// a NaN is), never as a large finite value
+// e4m3 of x * inv, round to nearest even.  The scale leaves every finite value at or below 448, so
+// the conversion's saturation never acts on one; e4m3 has no infinity, so +-inf is stored as NaN
+// (as a NaN is), never as a large finite value: callers whose row holds one pass it through
+// inf_to_nan.
+__device__ __forceinline__ float inf_to_nan(float x) { return fabsf(x) <= 3.402823466e38f ? x : __int_as_float(0x7fffffff); }
 __device__ __forceinline__ uint8_t to_e4m3(float x, float inv) {
-  return (uint8_t)__nv_cvt_float_to_fp8(x * inv, __NV_NOSAT, __NV_E4M3);
+  return (uint8_t)__nv_cvt_float_to_fp8(inf_to_nan(x) * inv, __NV_SATFINITE, __NV_E4M3);
 }
 __device__ __forceinline__ uint32_t to_e4m3x4(float a, float b, float c, float d, float inv) {
-  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a * inv, b * inv), __NV_NOSAT, __NV_E4M3);
-  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c * inv, d * inv), __NV_NOSAT, __NV_E4M3);
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a * inv, b * inv), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c * inv, d * inv), __NV_SATFINITE, __NV_E4M3);
   return lo | (hi << 16);
 }
 __device__ __forceinline__ float e4m3_f(uint8_t q) {
