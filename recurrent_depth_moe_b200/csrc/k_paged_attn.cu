@@ -100,17 +100,17 @@ __device__ __forceinline__ long long piece_of(long long length, int workers, int
 // ------------------------------------------------------------------------------------------
 // parts of a head group: m, l per head and o per head and channel, fp32
 // ------------------------------------------------------------------------------------------
-// Worker i leaves part 0 of the group it enters in the middle and part 1 of the one it begins
-// and does not finish, and in desc[i] the group it enters in the middle and finishes: it is the
-// last of the workers first .. i that share it.
+// CTA i leaves part 0 of the group it enters in the middle and part 1 of the one it begins and
+// does not finish, and in desc[i] the group it enters in the middle and finishes: it is the
+// last of the CTAs first .. i that share it.  (Behind the CTAs' parts lie those of their warps.)
 struct Desc {
   int b, seg, first, pad;
 };
-__device__ __forceinline__ float* part_ml(const PagedAttnParams& p, int worker, int which) {
-  return p.part_ml + ((long long)worker * 2 + which) * GT * 2;
+__device__ __forceinline__ float* part_ml(const PagedAttnParams& p, int at, int which) {
+  return p.part_ml + ((long long)at * 2 + which) * GT * 2;
 }
-__device__ __forceinline__ float* part_o(const PagedAttnParams& p, int worker, int which) {
-  return p.part_o + ((long long)worker * 2 + which) * GT * p.c.hd;
+__device__ __forceinline__ float* part_o(const PagedAttnParams& p, int at, int which) {
+  return p.part_o + ((long long)at * 2 + which) * GT * p.c.hd;
 }
 __device__ __forceinline__ Desc* desc_of(const PagedAttnParams& p) { return reinterpret_cast<Desc*>(p.scratch); }
 __device__ __forceinline__ void zero_rows(const PagedAttnParams& p, const Lens& lens, int es) {
@@ -126,14 +126,16 @@ __device__ __forceinline__ void let_join_start() { asm volatile("griddepcontrol.
 // tensor-core kernel
 // ------------------------------------------------------------------------------------------
 namespace {
-// Keys of a tile and ring stages: K and V of a tile are 8 KB at 128 channels.
-template <bool Q> struct Tile { static constexpr int KEYS = Q ? 32 : 16; };
-constexpr int STAGES = 3;
+// Keys of a tile (K and V are 8 KB at 128 channels), ring stages and CTAs on an SM.  bf16 waits
+// for memory, so it takes the deeper ring (105 us against 110 with 2 and 3, one sequence of
+// 131,071 keys); e4m3 issues twice the instructions a byte and takes more warps (313 us against
+// 342, 128 sequences of 4097 to 8191 keys).
+template <bool Q> struct Tile { static constexpr int KEYS = Q ? 32 : 16, STAGES = Q ? 2 : 3, CTAS = Q ? 3 : 2; };
 
 template <int HD, bool Q> struct Ring {    // HD: the head width rounded up to 64, 128 or 256
   static constexpr int ROW = HD * (Q ? 1 : 2);                  // bytes of a row
   static constexpr int STAGE = 2 * Tile<Q>::KEYS * ROW;         // K then V
-  static constexpr int BYTES = STAGES * STAGE;                  // of a warp
+  static constexpr int BYTES = Tile<Q>::STAGES * STAGE;         // of a warp
 };
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool valid) {
@@ -193,9 +195,9 @@ template <int PIECES> __device__ __forceinline__ int swz_v(int r, int c) {
 // 2^d, d <= 0; below the smallest normal value: nothing
 __device__ __forceinline__ float pow2_down(int d) { return d < -126 ? 0.f : __int_as_float((127 + d) << 23); }
 
-template <int HD, bool Q>
-__global__ void __launch_bounds__(32 * WARPS, HD <= 128 ? 2 : 1) k_paged_attn_mma(PagedAttnParams p, int least) {
-  constexpr int KEYS = Tile<Q>::KEYS, ROW = Ring<HD, Q>::ROW, STAGE = Ring<HD, Q>::STAGE;
+template <int HD, bool Q, bool UNI>
+__global__ void __launch_bounds__(32 * WARPS, HD <= 128 ? Tile<Q>::CTAS : 1) k_paged_attn_mma(PagedAttnParams p, int least) {
+  constexpr int KEYS = Tile<Q>::KEYS, STAGES = Tile<Q>::STAGES, ROW = Ring<HD, Q>::ROW, STAGE = Ring<HD, Q>::STAGE;
   constexpr int NG = KEYS / 8;                        // groups of 8 keys
   constexpr int PIECES = ROW / 16, EPP = Q ? 16 : 8;  // 16-byte pieces of a row, elements of a piece
   constexpr int QR = HD / 16;                         // k16 steps of a score
@@ -204,6 +206,8 @@ __global__ void __launch_bounds__(32 * WARPS, HD <= 128 ? 2 : 1) k_paged_attn_mm
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ long long red[WARPS];
   __shared__ int kept[LENS];
+  __shared__ long long run_id[2 * WARPS];             // the groups of the warps' parts, -1: none
+  __shared__ int run_end[WARPS], run_first[WARPS];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, j4 = lane & 3, n8 = lane >> 2;
   const int hd = p.c.hd, Hkv = p.c.Hkv, G = p.H / Hkv, n_ht = (G + GT - 1) / GT, segs = Hkv * n_ht;
   const int ps = p.c.page_size, row_bytes = hd * (Q ? 1 : 2), pieces = row_bytes / 16;
@@ -220,11 +224,98 @@ __global__ void __launch_bounds__(32 * WARPS, HD <= 128 ? 2 : 1) k_paged_attn_mm
   if (pieces < PIECES)
     for (int i = lane; i < Ring<HD, Q>::BYTES / 16; i += 32) reinterpret_cast<uint4*>(ring)[i] = make_uint4(0, 0, 0, 0);
   __syncwarp();
-  Desc joins{-1, 0, 0, 0};
-  Place at = w0 < w1 ? line_find(lens, segs, KEYS, w0) : Place{0, 0};
+  if (lane < 2) run_id[2 * warp + lane] = -1;
+  const Place start = w0 < w1 ? line_find(lens, segs, KEYS, w0) : Place{0, 0};
+
+  // ---- loading: the tiles of w0 .. w1 - 1 one after another, whatever group they belong to,
+  // STAGES - 1 ahead of the products.  Lane r holds the slot of key r of the tile to issue.
+  // UNI: pages hold whole groups of 16 keys, so a group's rows lie one after another.
+  long long ix = w0;
+  int ib = start.b, ilen = 0, int_ = 0, iseg = 0, it = 0, ig = 0, ist = 0;
+  if (w0 < w1) {
+    ilen = lens.keys(ib);
+    int_ = (ilen + KEYS - 1) / KEYS;
+    iseg = (int)(start.at / int_);
+    it = (int)(start.at % int_);
+    ig = iseg / n_ht;
+  }
+  auto slot_of = [&]() -> long long {
+    const int key = it * KEYS + lane;
+    if (ix >= w1 || lane >= KEYS || key >= ilen) return -1;
+    const int page = page_of(p.c, ib, key, p.st, 222);
+    return page < 0 ? -1 : ((long long)page * Hkv + ig) * ps + key % ps;
+  };
+  long long slot_n = slot_of();
+  int ke_r[STAGES], ve_r[STAGES];                     // e4m3: exponent bytes of the lane's key; [0]: of the tile in hand
+  unsigned ok_r[STAGES];                              // keys that take part
+#pragma unroll
+  for (int i = 0; i < STAGES; ++i) ke_r[i] = ve_r[i] = 0, ok_r[i] = 0;
+  auto issue = [&](int& ke, int& ve, unsigned& ok) {
+    const long long slot = slot_n;
+    ok = __ballot_sync(0xffffffffu, slot >= 0);
+    if (ix < w1) {
+      const uint32_t ka = ring_a + ist * STAGE, va = ka + KEYS * ROW;
+      const long long mine = slot * row_bytes;
+      // each row's pieces by neighbouring lanes
+      if (UNI) {
+        constexpr int RPI = 32 / PIECES;              // rows of one round
+        const int r0 = lane / PIECES, c = lane % PIECES;
+#pragma unroll
+        for (int gr = 0; gr < KEYS; gr += 16) {
+          const long long base = __shfl_sync(0xffffffffu, mine, gr);
+          const char* kp = (const char*)p.c.k + base + r0 * row_bytes + c * 16;
+          const char* vp = (const char*)p.c.v + base + r0 * row_bytes + c * 16;
+          const uint32_t okg = ok >> (gr + r0);
+          if (c < pieces) {
+#pragma unroll
+            for (int i = 0; i < 16 / RPI; ++i) {
+              const int r = gr + i * RPI + r0;
+              const bool in = okg >> (i * RPI) & 1;
+              cp16(ka + r * ROW + swz_k<PIECES>(r, c) * 16, in ? kp + i * RPI * row_bytes : (const char*)p.c.k, in);
+              cp16(va + r * ROW + swz_v<PIECES>(r, c) * 16, in ? vp + i * RPI * row_bytes : (const char*)p.c.v, in);
+            }
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i0 = 0; i0 < KEYS * PIECES; i0 += 32) {
+          const int i = i0 + lane, r = i / PIECES, c = i % PIECES;
+          const long long s = __shfl_sync(0xffffffffu, mine, r);
+          if (c < pieces) {
+            const long long off = s >= 0 ? s + c * 16 : 0;
+            cp16(ka + r * ROW + swz_k<PIECES>(r, c) * 16, (const char*)p.c.k + off, s >= 0);
+            cp16(va + r * ROW + swz_v<PIECES>(r, c) * 16, (const char*)p.c.v + off, s >= 0);
+          }
+        }
+      }
+      if (Q && slot >= 0) {
+        ke = __ldg(p.c.ke + slot);
+        ve = __ldg(p.c.ve + slot);
+      }
+      ist = ist + 1 == STAGES ? 0 : ist + 1;
+      ++ix;
+      if (++it == int_ && ix < w1) {                  // the next group
+        it = 0;
+        if (++iseg == segs) {
+          iseg = 0;
+          do ilen = lens.keys(++ib);
+          while (ilen == 0 && ib + 1 < p.B);
+          int_ = (ilen + KEYS - 1) / KEYS;
+        }
+        ig = iseg / n_ht;
+      }
+    }
+    cp_commit();
+    slot_n = slot_of();
+  };
+#pragma unroll
+  for (int i = 0; i < STAGES - 1; ++i) issue(ke_r[i], ve_r[i], ok_r[i]);
+
+  Place at = start;
+  int st = 0;
   for (long long x = w0; x < w1;) {
     // ---- one (sequence, head group): tiles t0 .. t1 - 1 of its nt
-    const int b = at.b, len = lens.keys(b), nt = (len + KEYS - 1) / KEYS;
+    const int b = at.b, nt = lens.tiles(b, KEYS);
     if (at.at >= (long long)nt * segs) {
       at = Place{b + 1, 0};
       continue;
@@ -277,55 +368,13 @@ __global__ void __launch_bounds__(32 * WARPS, HD <= 128 ? 2 : 1) k_paged_attn_mm
 #pragma unroll
     for (int i = 0; i < NC; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
 
-    // ---- the cache's tiles, two ahead.  Lane r holds the slot of key r of the tile to issue.
-    auto slot_of = [&](int t) -> long long {
-      const int key = t * KEYS + lane;
-      if (lane >= KEYS || t >= t1 || key >= len) return -1;
-      const int page = page_of(p.c, b, key, p.st, 222);
-      return page < 0 ? -1 : ((long long)page * Hkv + g) * ps + key % ps;
-    };
-    long long slot_n = slot_of(t0);                   // of the next tile to issue
-    int ke_r[STAGES], ve_r[STAGES];                   // e4m3: exponents of lane's key, by stage (rotated)
-    unsigned ok_r[STAGES];                            // keys of a stage that take part
-#pragma unroll
-    for (int i = 0; i < STAGES; ++i) ke_r[i] = ve_r[i] = 0, ok_r[i] = 0;
-    auto issue = [&](int t, int st, int& ke, int& ve, unsigned& ok) {
-      const long long slot = slot_n;
-      ok = __ballot_sync(0xffffffffu, slot >= 0);
-      if (t < t1) {
-        const uint32_t ka = ring_a + st * STAGE, va = ka + KEYS * ROW;
-        // each row's pieces by neighbouring lanes
-#pragma unroll
-        for (int i0 = 0; i0 < KEYS * PIECES; i0 += 32) {
-          const int i = i0 + lane, r = i / PIECES, c = i % PIECES;
-          const long long s = __shfl_sync(0xffffffffu, slot, r);
-          if (c < pieces) {
-            const long long off = s >= 0 ? s * row_bytes + c * 16 : 0;
-            cp16(ka + r * ROW + swz_k<PIECES>(r, c) * 16, (const char*)p.c.k + off, s >= 0);
-            cp16(va + r * ROW + swz_v<PIECES>(r, c) * 16, (const char*)p.c.v + off, s >= 0);
-          }
-        }
-        if (Q && slot >= 0) {
-          ke = __ldg(p.c.ke + slot);
-          ve = __ldg(p.c.ve + slot);
-        }
-      }
-      cp_commit();
-      slot_n = slot_of(t + 1);
-    };
-#pragma unroll
-    for (int i = 0; i < STAGES - 1; ++i) issue(t0 + i, i, ke_r[i], ve_r[i], ok_r[i]);
-    for (int tb = t0; tb < t1; tb += STAGES) {
-#pragma unroll
-      for (int st = 0; st < STAGES; ++st) {
-        const int t = tb + st;
-        if (t >= t1) break;
-        issue(t + STAGES - 1, (st + STAGES - 1) % STAGES, ke_r[(st + STAGES - 1) % STAGES], ve_r[(st + STAGES - 1) % STAGES],
-              ok_r[(st + STAGES - 1) % STAGES]);
+    for (int t = t0; t < t1; ++t) {
+        issue(ke_r[STAGES - 1], ve_r[STAGES - 1], ok_r[STAGES - 1]);
         cp_wait<STAGES - 1>();
         __syncwarp();
         const uint32_t ka = ring_a + st * STAGE, va = ka + KEYS * ROW;
-        const unsigned ok = ok_r[st];
+        const unsigned ok = ok_r[0];
+        st = st + 1 == STAGES ? 0 : st + 1;
         // scores of head n8, keys 8 g + 2 j4, + 1
         float sc[NG][4];
 #pragma unroll
@@ -346,47 +395,55 @@ __global__ void __launch_bounds__(32 * WARPS, HD <= 128 ? 2 : 1) k_paged_attn_mm
             }
           }
         }
+        // e4m3: lane r turns its key's exponents into the factors of the score and of the weight
+        float kf = 0.f, vf = 0.f, shrink = 1.f;
+        if (Q) {
+          const bool mine = ok >> lane & 1;
+          const int top = max(vexp, (int)__reduce_max_sync(0xffffffffu, mine ? ve_r[0] - 127 : -128));
+          kf = exp_byte_scale(ke_r[0]);
+          vf = mine ? pow2_down(ve_r[0] - 127 - top) : 0.f;
+          shrink = pow2_down(vexp - top);
+          vexp = top;
+        }
         float mx = -INFINITY;
 #pragma unroll
         for (int kg = 0; kg < NG; ++kg)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const int r = kg * 8 + 2 * j4 + e;
-            float f = sl2;
-            if (Q) f *= exp_byte_scale(__shfl_sync(0xffffffffu, ke_r[st], r));
-            const float s = (ok >> r & 1) ? sc[kg][e] * f : -INFINITY;
-            sc[kg][e] = s;
-            mx = s > mx || s != s ? s : mx;             // a NaN score makes the row NaN
+            sc[kg][e] *= Q ? sl2 * __shfl_sync(0xffffffffu, kf, kg * 8 + 2 * j4 + e) : sl2;
+            mx = fmaxf(mx, sc[kg][e]);
           }
+        if (ok != (KEYS == 32 ? 0xffffffffu : (1u << KEYS % 32) - 1)) {   // the last tile, or a bad page
+          mx = -INFINITY;
+#pragma unroll
+          for (int kg = 0; kg < NG; ++kg)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              if (!(ok >> (kg * 8 + 2 * j4 + e) & 1)) sc[kg][e] = -INFINITY;
+              mx = fmaxf(mx, sc[kg][e]);
+            }
+        }
+        // (a NaN score drops out of the maximum, and its weight makes the sums NaN)
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
         const float mn = fmaxf(m, mx), base = mn == -INFINITY ? 0.f : mn;
-        float corr = ex2(m - base);
+        const float corr = ex2(m - base);
         m = mn;
-        int ve_max = vexp;
-        if (Q) ve_max = max(vexp, (int)__reduce_max_sync(0xffffffffu, (ok >> lane & 1) ? ve_r[st] : -1) - 127);
-        const float shrink = Q ? pow2_down(vexp - ve_max) : 1.f;
-        vexp = ve_max;
-        if (__any_sync(0xffffffffu, corr != 1.f || shrink != 1.f)) {
+        if (__any_sync(0xffffffffu, corr != 1.f) || (Q && shrink != 1.f)) {
           const float f = corr * shrink;
+          l *= corr;
 #pragma unroll
           for (int i = 0; i < NC; ++i) acc[i][0] *= f, acc[i][1] *= f, acc[i][2] *= f, acc[i][3] *= f;
         }
-        l *= corr;
         uint32_t ph[NG], pl[NG];                        // weights of keys 8 g + 2 j4, + 1
 #pragma unroll
         for (int kg = 0; kg < NG; ++kg) {
           float w[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float x = ex2(sc[kg][e] - base);
-            l += x;                                     // this lane's keys; the 4 lanes are summed at the end
-            w[e] = x;
-            if (Q) {
-              const int r = kg * 8 + 2 * j4 + e;
-              const int ve = __shfl_sync(0xffffffffu, ve_r[st], r);
-              w[e] = (ok >> r & 1) ? x * pow2_down(ve - 127 - vexp) : 0.f;
-            }
+            w[e] = ex2(sc[kg][e] - base);
+            l += w[e];                                  // this lane's keys; the 4 lanes are summed at the end
+            if (Q) w[e] *= __shfl_sync(0xffffffffu, vf, kg * 8 + 2 * j4 + e);
           }
           split2<Q>(w[0], w[1], ph[kg], pl[kg]);
         }
@@ -424,9 +481,9 @@ __global__ void __launch_bounds__(32 * WARPS, HD <= 128 ? 2 : 1) k_paged_attn_mm
             }
           }
         __syncwarp();                                   // the stage is free to be written
-      }
+#pragma unroll
+        for (int i = 0; i + 1 < STAGES; ++i) ke_r[i] = ke_r[i + 1], ve_r[i] = ve_r[i + 1], ok_r[i] = ok_r[i + 1];
     }
-    cp_wait<0>();
     l += __shfl_xor_sync(0xffffffffu, l, 1);
     l += __shfl_xor_sync(0xffffffffu, l, 2);
     const float back = Q ? ldexpf(1.f, vexp) : 1.f;
@@ -459,9 +516,12 @@ __global__ void __launch_bounds__(32 * WARPS, HD <= 128 ? 2 : 1) k_paged_attn_mm
           }
     } else {
       const int which = t0 == 0;
-      if (t0 > 0 && t1 == nt) joins = Desc{b, seg, (int)((x - t0) / piece), 0};
-      float* ml = part_ml(p, worker, which);
-      float* po = part_o(p, worker, which) + n8 * hd;
+      if (lane == 0) {
+        run_id[2 * warp + which] = (long long)b * segs + seg;
+        if (which == 0) run_end[warp] = t1 == nt, run_first[warp] = (int)((x - t0) / (piece * WARPS));
+      }
+      float* ml = part_ml(p, gridDim.x + worker, which);
+      float* po = part_o(p, gridDim.x + worker, which) + n8 * hd;
       if (j4 == 0) {
         ml[n8 * 2] = m;
         ml[n8 * 2 + 1] = l;
@@ -487,7 +547,56 @@ __global__ void __launch_bounds__(32 * WARPS, HD <= 128 ? 2 : 1) k_paged_attn_mm
     x += t1 - t0;
     at.at += t1 - t0;
   }
-  if (lane == 0) desc_of(p)[worker] = joins;
+  // ---- the warps' parts of one group, neighbours in the order (entered, left) of the warps,
+  // become the output if the group lies within the CTA, else the CTA's part
+  __syncthreads();
+  Desc joins{-1, 0, 0, 0};
+  for (int i = 0; i < 2 * WARPS;) {
+    const long long id = run_id[i];
+    if (id < 0) {
+      ++i;
+      continue;
+    }
+    int last = i, j = i + 1;
+    for (; j < 2 * WARPS && (run_id[j] < 0 || run_id[j] == id); ++j)
+      if (run_id[j] == id) last = j;
+    const bool begun = i & 1, ended = !(last & 1) && run_end[last >> 1];   // within this CTA
+    const int b = (int)(id / segs), seg = (int)(id % segs), g = seg / n_ht, h0 = seg % n_ht * GT, nh = min(GT, G - h0);
+    if (!begun && ended) joins = Desc{b, seg, run_first[last >> 1], 0};
+    for (int h = 0; h < nh; ++h) {
+      float M = -INFINITY, L = 0.f, w[2 * WARPS];
+#pragma unroll
+      for (int k = 0; k < 2 * WARPS; ++k) {
+        const bool in = k >= i && k <= last && run_id[k] == id;
+        w[k] = in ? part_ml(p, gridDim.x + blockIdx.x * WARPS + (k >> 1), k & 1)[h * 2] : -INFINITY;
+        M = fmaxf(M, w[k]);
+      }
+      const float base = M == -INFINITY ? 0.f : M;
+#pragma unroll
+      for (int k = 0; k < 2 * WARPS; ++k) {
+        const bool in = k >= i && k <= last && run_id[k] == id;
+        w[k] = in ? ex2(w[k] - base) : 0.f;
+        if (in) L += w[k] * part_ml(p, gridDim.x + blockIdx.x * WARPS + (k >> 1), k & 1)[h * 2 + 1];
+      }
+      for (int ch = threadIdx.x; ch < hd; ch += 32 * WARPS) {
+        float o = 0.f;
+#pragma unroll
+        for (int k = 0; k < 2 * WARPS; ++k)
+          if (k >= i && k <= last && run_id[k] == id)
+            o = fmaf(w[k], part_o(p, gridDim.x + blockIdx.x * WARPS + (k >> 1), k & 1)[h * hd + ch], o);
+        if (begun && ended)
+          ((bf16*)p.o)[(long long)b * p.o_row + (long long)(g * G + h0 + h) * hd + ch] = from_f<bf16>(L != 0.f ? o / L : 0.f);
+        else
+          part_o(p, blockIdx.x, begun)[h * hd + ch] = o;
+      }
+      if (threadIdx.x == 0 && !(begun && ended)) {
+        part_ml(p, blockIdx.x, begun)[h * 2] = M;
+        part_ml(p, blockIdx.x, begun)[h * 2 + 1] = L;
+      }
+    }
+    i = j;
+  }
+  if (threadIdx.x == 0) desc_of(p)[blockIdx.x] = joins;
   let_join_start();
 }
 
@@ -713,51 +822,64 @@ __global__ void __launch_bounds__(128) k_paged_attn_simt(PagedAttnParams p, int 
 }
 
 // ------------------------------------------------------------------------------------------
-// join: CTA i joins the parts of the group that worker i finished
+// join: the parts of the group that CTA i finished
 // ------------------------------------------------------------------------------------------
-// 512 threads: 4 slices of the parts, 128 channels each; weights in shared memory.
-constexpr int JT = 512;
+// CTA (i, head): 4 warps take slices of the parts, a lane four channels (of each 128).
 template <typename T>
-__global__ void __launch_bounds__(JT) k_paged_attn_join(PagedAttnParams p) {
-  extern __shared__ float wj[];                       // [parts] 2^(m - M) of one head
-  __shared__ float red[JT / 32], sum[JT / 128][128];
+__global__ void __launch_bounds__(128) k_paged_attn_join(PagedAttnParams p) {
+  extern __shared__ float wj[];                       // [parts] 2^(m - M)
+  __shared__ float red[WARPS];
+  __shared__ __align__(16) float4 sum[WARPS][32];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Desc d = desc_of(p)[blockIdx.x];
   if (d.b < 0) return;
-  const int hd = p.c.hd, G = p.H / p.c.Hkv, n_ht = (G + GT - 1) / GT;
-  const int g = d.seg / n_ht, h0 = d.seg % n_ht * GT, nh = min(GT, G - h0), n = (int)blockIdx.x - d.first + 1;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, slice = tid >> 7, c = tid & 127;
-  // part 1 of the first worker, part 0 of the others
-  for (int h = 0; h < nh; ++h) {
-    float M = -INFINITY, L = 0.f;
-    for (int s = tid; s < n; s += JT) M = fmaxf(M, part_ml(p, d.first + s, s == 0)[h * 2]);
-    M = warp_max(M);
-    __syncthreads();
-    if (lane == 0) red[warp] = M;
-    __syncthreads();
-    M = warp_max(lane < JT / 32 ? red[lane] : -INFINITY);
-    const float base = M == -INFINITY ? 0.f : M;
-    for (int s = tid; s < n; s += JT) {
-      const float* ml = part_ml(p, d.first + s, s == 0);
-      const float w = exp2f(ml[h * 2] - base);
-      wj[s] = w;
-      L += w * ml[h * 2 + 1];
-    }
-    L = block_sum(L, red);                            // (its barriers also cover wj)
+  const int hd = p.c.hd, G = p.H / p.c.Hkv, n_ht = (G + GT - 1) / GT, h = blockIdx.y;
+  const int g = d.seg / n_ht, h0 = d.seg % n_ht * GT, n = (int)blockIdx.x - d.first + 1;
+  if (h >= min(GT, G - h0)) return;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // part 1 of the first CTA, part 0 of the others
+  float M = -INFINITY, L = 0.f;
+  for (int s = tid; s < n; s += 128) M = fmaxf(M, part_ml(p, d.first + s, s == 0)[h * 2]);
+  M = warp_max(M);
+  if (lane == 0) red[warp] = M;
+  __syncthreads();
+  M = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  const float base = M == -INFINITY ? 0.f : M;
+  for (int s = tid; s < n; s += 128) {
+    const float* ml = part_ml(p, d.first + s, s == 0);
+    const float w = exp2f(ml[h * 2] - base);
+    wj[s] = w;
+    L += w * ml[h * 2 + 1];
+  }
+  __syncthreads();
+  L = block_sum(L, red);
+  const float inv = L != 0.f ? 1.f / L : 0.f;
+  T* o = (T*)p.o + (long long)d.b * p.o_row + (long long)(g * G + h0 + h) * hd;
+  if (hd % 4 == 0) {
     for (int ch0 = 0; ch0 < hd; ch0 += 128) {
-      const int ch = ch0 + c;
-      float o = 0.f;
+      const int ch = ch0 + 4 * lane;
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
       if (ch < hd) {
 #pragma unroll 8
-        for (int s = slice; s < n; s += JT / 128) o = fmaf(wj[s], part_o(p, d.first + s, s == 0)[h * hd + ch], o);
+        for (int s = warp; s < n; s += WARPS) {
+          const float4 x = *reinterpret_cast<const float4*>(part_o(p, d.first + s, s == 0) + h * hd + ch);
+          const float w = wj[s];
+          a.x = fmaf(w, x.x, a.x); a.y = fmaf(w, x.y, a.y); a.z = fmaf(w, x.z, a.z); a.w = fmaf(w, x.w, a.w);
+        }
       }
-      sum[slice][c] = o;
+      sum[warp][lane] = a;
       __syncthreads();
-      if (slice == 0 && ch < hd) {
-        o = (sum[0][c] + sum[1][c]) + (sum[2][c] + sum[3][c]);
-        ((T*)p.o)[(long long)d.b * p.o_row + (long long)(g * G + h0 + h) * hd + ch] = from_f<T>(L != 0.f ? o / L : 0.f);
+      if (ch0 + tid < hd) {
+        const float* f = reinterpret_cast<const float*>(&sum[0][0]);
+        o[ch0 + tid] = from_f<T>(((f[tid] + f[128 + tid]) + (f[256 + tid] + f[384 + tid])) * inv);
       }
       __syncthreads();
+    }
+  } else {
+    for (int ch = tid; ch < hd; ch += 128) {
+      float a = 0.f;
+      for (int s = 0; s < n; ++s) a = fmaf(wj[s], part_o(p, d.first + s, s == 0)[h * hd + ch], a);
+      o[ch] = from_f<T>(a * inv);
     }
   }
 }
@@ -771,15 +893,18 @@ bool mma_takes(int dtype, const PagedView& c) {
   const int rb = c.hd * (c.e4m3 ? 1 : 2);
   return dtype == 1 && c.hd % 8 == 0 && rb % 16 == 0 && !(((uintptr_t)c.k | (uintptr_t)c.v) & 15);
 }
-int workers_mma() { return device_sm_count() * 2 * WARPS; }
-int workers_simt() { return device_sm_count() * 4; }
-size_t scratch_bytes(int workers, int hd) { return (size_t)workers * (sizeof(Desc) + 2 * GT * (hd + 2) * sizeof(float)); }
+int ctas_mma(bool e4m3) { return device_sm_count() * (e4m3 ? Tile<true>::CTAS : Tile<false>::CTAS); }
+int ctas_simt() { return device_sm_count() * 4; }
+// descriptors, then the parts of `ctas` CTAs and, on tensor cores, of their warps
+size_t scratch_bytes(int ctas, int parts, int hd) {
+  return (size_t)ctas * sizeof(Desc) + (size_t)parts * 2 * GT * (hd + 2) * sizeof(float);
+}
 
-template <typename T> int launch_join(const PagedAttnParams& p, int workers, cudaStream_t s) {
+template <typename T> int launch_join(const PagedAttnParams& p, int ctas, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)workers);
-  cfg.blockDim = dim3(JT);
-  cfg.dynamicSmemBytes = (size_t)workers * sizeof(float);
+  cfg.gridDim = dim3((unsigned)ctas, (unsigned)std::min(GT, p.H / p.c.Hkv));
+  cfg.blockDim = dim3(128);
+  cfg.dynamicSmemBytes = (size_t)ctas * sizeof(float);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // launched while the workers finish
@@ -792,19 +917,26 @@ template <typename T> int launch_join(const PagedAttnParams& p, int workers, cud
 }
 }  // namespace
 
-// The same for every batch and head count: the parts belong to the workers.
+// The same for every batch and head count: the parts belong to the CTAs.
 size_t paged_attn_scratch(const PagedView& c) {
-  return std::max(scratch_bytes(workers_mma(), c.hd), scratch_bytes(workers_simt(), c.hd));
+  const int n = ctas_mma(c.e4m3);
+  return std::max(scratch_bytes(n, n * (1 + WARPS), c.hd), scratch_bytes(ctas_simt(), ctas_simt(), c.hd));
 }
 
 int launch_paged_attn(int dtype, const PagedAttnParams& p0, cudaStream_t s) {
   PagedAttnParams p = p0;
   const bool tc = mma_takes(dtype, p.c);
-  const int workers = tc ? workers_mma() : workers_simt();
-  p.part_ml = reinterpret_cast<float*>((char*)p.scratch + (size_t)workers * sizeof(Desc));
-  p.part_o = p.part_ml + (size_t)workers * 2 * GT * 2;
+  const int ctas = tc ? ctas_mma(p.c.e4m3) : ctas_simt();
+  p.part_ml = reinterpret_cast<float*>((char*)p.scratch + (size_t)ctas * sizeof(Desc));
+  p.part_o = p.part_ml + (size_t)(tc ? ctas * (1 + WARPS) : ctas) * 2 * GT * 2;
   if (tc) {
-#define RDT_MMA(HD, QQ)                                                                                            do {                                                                                                               constexpr int smem = WARPS * Ring<HD, QQ>::BYTES;                                                                if (!ensure_smem_limit((const void*)k_paged_attn_mma<HD, QQ>, smem)) return -1;                                  k_paged_attn_mma<HD, QQ><<<workers / WARPS, 32 * WARPS, smem, s>>>(p, 2);                                      } while (0)
+#define RDT_MMA(HD, QQ)                                                                                     \
+  do {                                                                                                      \
+    constexpr int smem = WARPS * Ring<HD, QQ>::BYTES;                                                       \
+    auto kernel = p.c.page_size % 16 ? k_paged_attn_mma<HD, QQ, false> : k_paged_attn_mma<HD, QQ, true>;    \
+    if (!ensure_smem_limit((const void*)kernel, smem)) return -1;                                           \
+    kernel<<<ctas, 32 * WARPS, smem, s>>>(p, 2);                                                              \
+  } while (0)
     if (p.c.e4m3) {
       if (p.c.hd <= 64) RDT_MMA(64, true);
       else if (p.c.hd <= 128) RDT_MMA(128, true);
@@ -816,12 +948,12 @@ int launch_paged_attn(int dtype, const PagedAttnParams& p0, cudaStream_t s) {
     }
 #undef RDT_MMA
     note_launch();
-    return launch_join<bf16>(p, workers, s);
+    return launch_join<bf16>(p, ctas, s);
   }
   const int smem = (int)PlainSm::bytes(p.c.hd), most = (int)PlainSm::bytes(256);
   const int eb = p.c.e4m3 ? 1 : dtype == 0 ? 4 : 2;
   const int vec = p.c.hd % 4 == 0 && !(((uintptr_t)p.c.k | (uintptr_t)p.c.v) & (4 * eb - 1));
-#define RDT_SIMT(TT, QQ)                                                                      do {                                                                                          if (!ensure_smem_limit((const void*)k_paged_attn_simt<TT, QQ>, most)) return -1;            k_paged_attn_simt<TT, QQ><<<workers, 128, smem, s>>>(p, 1, vec);                          } while (0)
+#define RDT_SIMT(TT, QQ)                                                                      do {                                                                                          if (!ensure_smem_limit((const void*)k_paged_attn_simt<TT, QQ>, most)) return -1;            k_paged_attn_simt<TT, QQ><<<ctas, 128, smem, s>>>(p, 1, vec);                          } while (0)
   if (dtype == 0) {
     if (p.c.e4m3) RDT_SIMT(float, true);
     else RDT_SIMT(float, false);
@@ -831,7 +963,7 @@ int launch_paged_attn(int dtype, const PagedAttnParams& p0, cudaStream_t s) {
   }
 #undef RDT_SIMT
   note_launch();
-  return dtype == 0 ? launch_join<float>(p, workers, s) : launch_join<bf16>(p, workers, s);
+  return dtype == 0 ? launch_join<float>(p, ctas, s) : launch_join<bf16>(p, ctas, s);
 }
 
 }  // namespace rdt
