@@ -43,13 +43,19 @@ __device__ __forceinline__ float ex2(float x) {
 // ------------------------------------------------------------------------------------------
 // the line of work
 // ------------------------------------------------------------------------------------------
-// Units per sequence: ceil(keys / tile) tiles for each of `segs` (kv head, head group) pairs.
+// Units per sequence: ceil(keys / tile) tiles, and START for what a group costs beside them, for
+// each of `segs` (kv head, head group) pairs; tile t is unit START + t of its group.
+constexpr int START = 2;
 constexpr int LENS = 512;           // lengths kept in shared memory (of a longer batch: none)
 struct Lens {
   const PagedAttnParams& p;
   const int* kept;                  // shared memory, or null
   __device__ __forceinline__ int keys(int b) const { return kept ? kept[b] : visible_keys(p.c, p.lens, b, p.len_add, nullptr, 0); }
   __device__ __forceinline__ int tiles(int b, int tile) const { return (keys(b) + tile - 1) / tile; }
+  __device__ __forceinline__ int units(int b, int tile) const {
+    const int n = tiles(b, tile);
+    return n ? n + START : 0;
+  }
 };
 // Length of the line (all 128 threads of the CTA; keep: LENS ints, red: 4 words of shared memory).
 __device__ long long line_length(const PagedAttnParams& p, int segs, int tile, int* keep, long long* red) {
@@ -57,7 +63,7 @@ __device__ long long line_length(const PagedAttnParams& p, int segs, int tile, i
   for (int b = threadIdx.x; b < p.B; b += 128) {
     const int len = visible_keys(p.c, p.lens, b, p.len_add, p.st, 221);
     if (p.B <= LENS) keep[b] = len;
-    n += (long long)((len + tile - 1) / tile) * segs;
+    if (len > 0) n += (long long)((len + tile - 1) / tile + START) * segs;
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
@@ -75,7 +81,7 @@ __device__ __forceinline__ Place line_find(const Lens& lens, int segs, int tile,
   long long base = 0;
   for (int b0 = 0; b0 < lens.p.B; b0 += 32) {
     const int b = b0 + lane;
-    const long long n = b < lens.p.B ? (long long)lens.tiles(b, tile) * segs : 0;
+    const long long n = b < lens.p.B ? (long long)lens.units(b, tile) * segs : 0;
     long long c = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -235,8 +241,10 @@ __global__ void __launch_bounds__(32 * WARPS, HD <= 128 ? Tile<Q>::CTAS : 1) k_p
   if (w0 < w1) {
     ilen = lens.keys(ib);
     int_ = (ilen + KEYS - 1) / KEYS;
-    iseg = (int)(start.at / int_);
-    it = (int)(start.at % int_);
+    iseg = (int)(start.at / (int_ + START));
+    it = (int)(start.at % (int_ + START)) - START;
+    ix -= min(it, 0);                                 // (the line's place of the tile, START units counted)
+    it = max(it, 0);
     ig = iseg / n_ht;
   }
   auto slot_of = [&]() -> long long {
@@ -296,6 +304,7 @@ __global__ void __launch_bounds__(32 * WARPS, HD <= 128 ? Tile<Q>::CTAS : 1) k_p
       ++ix;
       if (++it == int_ && ix < w1) {                  // the next group
         it = 0;
+        ix += START;
         if (++iseg == segs) {
           iseg = 0;
           do ilen = lens.keys(++ib);
@@ -315,13 +324,17 @@ __global__ void __launch_bounds__(32 * WARPS, HD <= 128 ? Tile<Q>::CTAS : 1) k_p
   int st = 0;
   for (long long x = w0; x < w1;) {
     // ---- one (sequence, head group): tiles t0 .. t1 - 1 of its nt
-    const int b = at.b, nt = lens.tiles(b, KEYS);
-    if (at.at >= (long long)nt * segs) {
+    const int b = at.b, nt = lens.tiles(b, KEYS), nu = lens.units(b, KEYS);
+    if (at.at >= (long long)nu * segs) {
       at = Place{b + 1, 0};
       continue;
     }
-    const int seg = (int)(at.at / nt), t0 = (int)(at.at % nt);
-    const int t1 = nt - t0 < w1 - x ? nt : t0 + (int)(w1 - x);
+    const int seg = (int)(at.at / nu), u0 = (int)(at.at % nu), u1 = nu - u0 < w1 - x ? nu : u0 + (int)(w1 - x);
+    const int t0 = max(u0 - START, 0), t1 = max(u1 - START, 0);
+    const long long begin = x - u0;                   // the group's first unit
+    x += u1 - u0;
+    at.at += u1 - u0;
+    if (t0 == t1) continue;
     const int g = seg / n_ht, h0 = seg % n_ht * GT, nh = min(GT, G - h0);
     float m = -INFINITY, l = 0.f;                     // of head n8; l: this lane's keys
     float acc[NC][4];                                 // [channel group]: rows n8 (upper words), n8 + 8 (lower)
@@ -518,7 +531,7 @@ __global__ void __launch_bounds__(32 * WARPS, HD <= 128 ? Tile<Q>::CTAS : 1) k_p
       const int which = t0 == 0;
       if (lane == 0) {
         run_id[2 * warp + which] = (long long)b * segs + seg;
-        if (which == 0) run_end[warp] = t1 == nt, run_first[warp] = (int)((x - t0) / (piece * WARPS));
+        if (which == 0) run_end[warp] = t1 == nt, run_first[warp] = (int)((begin + START) / (piece * WARPS));
       }
       float* ml = part_ml(p, gridDim.x + worker, which);
       float* po = part_o(p, gridDim.x + worker, which) + n8 * hd;
@@ -544,8 +557,6 @@ __global__ void __launch_bounds__(32 * WARPS, HD <= 128 ? Tile<Q>::CTAS : 1) k_p
             }
           }
     }
-    x += t1 - t0;
-    at.at += t1 - t0;
   }
   // ---- the warps' parts of one group, neighbours in the order (entered, left) of the warps,
   // become the output if the group lies within the CTA, else the CTA's part
@@ -651,13 +662,17 @@ __global__ void __launch_bounds__(128) k_paged_attn_simt(PagedAttnParams p, int 
   Desc joins{-1, 0, 0, 0};
   Place at = w0 < w1 ? line_find(lens, segs, TK, w0) : Place{0, 0};
   for (long long x = w0; x < w1;) {
-    const int b = at.b, len = lens.keys(b), nt = (len + TK - 1) / TK;
-    if (at.at >= (long long)nt * segs) {
+    const int b = at.b, len = lens.keys(b), nt = lens.tiles(b, TK), nu = lens.units(b, TK);
+    if (at.at >= (long long)nu * segs) {
       at = Place{b + 1, 0};
       continue;
     }
-    const int seg = (int)(at.at / nt), t0 = (int)(at.at % nt);
-    const int t1 = nt - t0 < w1 - x ? nt : t0 + (int)(w1 - x);
+    const int seg = (int)(at.at / nu), u0 = (int)(at.at % nu), u1 = nu - u0 < w1 - x ? nu : u0 + (int)(w1 - x);
+    const int t0 = max(u0 - START, 0), t1 = max(u1 - START, 0);
+    const long long begin = x - u0;                   // the group's first unit
+    x += u1 - u0;
+    at.at += u1 - u0;
+    if (t0 == t1) continue;
     const int g = seg / n_ht, h0 = seg % n_ht * GT, nh = min(GT, G - h0);
     const float sl2 = p.scale * LOG2E;
     __syncthreads();
@@ -785,7 +800,7 @@ __global__ void __launch_bounds__(128) k_paged_attn_simt(PagedAttnParams p, int 
     }
     const bool whole = t0 == 0 && t1 == nt;
     const int which = t0 == 0;
-    if (t0 > 0 && t1 == nt) joins = Desc{b, seg, (int)((x - t0) / piece), 0};
+    if (t0 > 0 && t1 == nt) joins = Desc{b, seg, (int)((begin + START) / piece), 0};
     __syncthreads();
     if (lane == 0) {
 #pragma unroll
@@ -814,8 +829,6 @@ __global__ void __launch_bounds__(128) k_paged_attn_simt(PagedAttnParams p, int 
           part_o(p, blockIdx.x, which)[h * hd + d] = acc[h][u];
       }
     }
-    x += t1 - t0;
-    at.at += t1 - t0;
   }
   if (tid == 0) desc_of(p)[blockIdx.x] = joins;
   let_join_start();
@@ -935,7 +948,7 @@ int launch_paged_attn(int dtype, const PagedAttnParams& p0, cudaStream_t s) {
     constexpr int smem = WARPS * Ring<HD, QQ>::BYTES;                                                       \
     auto kernel = p.c.page_size % 16 ? k_paged_attn_mma<HD, QQ, false> : k_paged_attn_mma<HD, QQ, true>;    \
     if (!ensure_smem_limit((const void*)kernel, smem)) return -1;                                           \
-    kernel<<<ctas, 32 * WARPS, smem, s>>>(p, 2);                                                              \
+    kernel<<<ctas, 32 * WARPS, smem, s>>>(p, 4);                                                              \
   } while (0)
     if (p.c.e4m3) {
       if (p.c.hd <= 64) RDT_MMA(64, true);
@@ -953,7 +966,7 @@ int launch_paged_attn(int dtype, const PagedAttnParams& p0, cudaStream_t s) {
   const int smem = (int)PlainSm::bytes(p.c.hd), most = (int)PlainSm::bytes(256);
   const int eb = p.c.e4m3 ? 1 : dtype == 0 ? 4 : 2;
   const int vec = p.c.hd % 4 == 0 && !(((uintptr_t)p.c.k | (uintptr_t)p.c.v) & (4 * eb - 1));
-#define RDT_SIMT(TT, QQ)                                                                      do {                                                                                          if (!ensure_smem_limit((const void*)k_paged_attn_simt<TT, QQ>, most)) return -1;            k_paged_attn_simt<TT, QQ><<<ctas, 128, smem, s>>>(p, 1, vec);                          } while (0)
+#define RDT_SIMT(TT, QQ)                                                                      do {                                                                                          if (!ensure_smem_limit((const void*)k_paged_attn_simt<TT, QQ>, most)) return -1;            k_paged_attn_simt<TT, QQ><<<ctas, 128, smem, s>>>(p, 3, vec);                          } while (0)
   if (dtype == 0) {
     if (p.c.e4m3) RDT_SIMT(float, true);
     else RDT_SIMT(float, false);
