@@ -144,7 +144,10 @@ template <int HD, bool Q> struct Ring {    // HD: the head width rounded up to 6
   static constexpr int BYTES = Tile<Q>::STAGES * STAGE;         // of a warp
 };
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool valid) {
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src));
+}
+__device__ __forceinline__ void cp16_or_zero(uint32_t dst, const void* src, bool valid) {
   const int n = valid ? 16 : 0;                                 // 0: zeros are written, nothing is read
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n));
 }
@@ -205,6 +208,7 @@ template <int HD, bool Q, bool UNI>
 __global__ void __launch_bounds__(32 * WARPS, HD <= 128 ? Tile<Q>::CTAS : 1) k_paged_attn_mma(PagedAttnParams p, int least) {
   constexpr int KEYS = Tile<Q>::KEYS, STAGES = Tile<Q>::STAGES, ROW = Ring<HD, Q>::ROW, STAGE = Ring<HD, Q>::STAGE;
   constexpr int NG = KEYS / 8;                        // groups of 8 keys
+  constexpr unsigned ALL = KEYS == 32 ? 0xffffffffu : (1u << KEYS % 32) - 1;
   constexpr int PIECES = ROW / 16, EPP = Q ? 16 : 8;  // 16-byte pieces of a row, elements of a piece
   constexpr int QR = HD / 16;                         // k16 steps of a score
   constexpr int VH = (PIECES + 7) / 8;                // pieces of a value row that one lane reads
@@ -236,22 +240,27 @@ __global__ void __launch_bounds__(32 * WARPS, HD <= 128 ? Tile<Q>::CTAS : 1) k_p
   // ---- loading: the tiles of w0 .. w1 - 1 one after another, whatever group they belong to,
   // STAGES - 1 ahead of the products.  Lane r holds the slot of key r of the tile to issue.
   // UNI: pages hold whole groups of 16 keys, so a group's rows lie one after another.
-  long long ix = w0;
-  int ib = start.b, ilen = 0, int_ = 0, iseg = 0, it = 0, ig = 0, ist = 0;
+  int left = (int)(w1 - w0), ib = start.b, ilen = 0, int_ = 0, iseg = 0, it = 0, ig = 0, ist = 0;   // left: units of the line
   if (w0 < w1) {
     ilen = lens.keys(ib);
     int_ = (ilen + KEYS - 1) / KEYS;
     iseg = (int)(start.at / (int_ + START));
     it = (int)(start.at % (int_ + START)) - START;
-    ix -= min(it, 0);                                 // (the line's place of the tile, START units counted)
+    left += min(it, 0);
     it = max(it, 0);
     ig = iseg / n_ht;
   }
+  const int* table = p.c.table + (long long)ib * p.c.max_pages;
   auto slot_of = [&]() -> long long {
     const int key = it * KEYS + lane;
-    if (ix >= w1 || lane >= KEYS || key >= ilen) return -1;
-    const int page = page_of(p.c, ib, key, p.st, 222);
-    return page < 0 ? -1 : ((long long)page * Hkv + ig) * ps + key % ps;
+    if (left <= 0 || lane >= KEYS || key >= ilen) return -1;   // (lengths are within the table)
+    const int pi = p.ps_shift >= 0 ? key >> p.ps_shift : key / ps;
+    const int page = __ldg(table + pi);
+    if ((unsigned)page >= (unsigned)p.c.n_pages) {
+      record_status(p.st, ST_BOUNDS, 222, page);
+      return -1;
+    }
+    return ((long long)page * Hkv + ig) * ps + (key - pi * ps);
   };
   long long slot_n = slot_of();
   int ke_r[STAGES], ve_r[STAGES];                     // e4m3: exponent bytes of the lane's key; [0]: of the tile in hand
@@ -261,26 +270,30 @@ __global__ void __launch_bounds__(32 * WARPS, HD <= 128 ? Tile<Q>::CTAS : 1) k_p
   auto issue = [&](int& ke, int& ve, unsigned& ok) {
     const long long slot = slot_n;
     ok = __ballot_sync(0xffffffffu, slot >= 0);
-    if (ix < w1) {
+    if (left > 0) {
       const uint32_t ka = ring_a + ist * STAGE, va = ka + KEYS * ROW;
       const long long mine = slot * row_bytes;
       // each row's pieces by neighbouring lanes
-      if (UNI) {
+      if (UNI && ok == ALL) {
         constexpr int RPI = 32 / PIECES;              // rows of one round
         const int r0 = lane / PIECES, c = lane % PIECES;
 #pragma unroll
         for (int gr = 0; gr < KEYS; gr += 16) {
-          const long long base = __shfl_sync(0xffffffffu, mine, gr);
-          const char* kp = (const char*)p.c.k + base + r0 * row_bytes + c * 16;
-          const char* vp = (const char*)p.c.v + base + r0 * row_bytes + c * 16;
-          const uint32_t okg = ok >> (gr + r0);
-          if (c < pieces) {
+          const long long off = __shfl_sync(0xffffffffu, mine, gr) + r0 * row_bytes + c * 16;
+          const char *kp = (const char*)p.c.k + off, *vp = (const char*)p.c.v + off;
+          if (pieces == PIECES) {                     // (known strides)
 #pragma unroll
             for (int i = 0; i < 16 / RPI; ++i) {
               const int r = gr + i * RPI + r0;
-              const bool in = okg >> (i * RPI) & 1;
-              cp16(ka + r * ROW + swz_k<PIECES>(r, c) * 16, in ? kp + i * RPI * row_bytes : (const char*)p.c.k, in);
-              cp16(va + r * ROW + swz_v<PIECES>(r, c) * 16, in ? vp + i * RPI * row_bytes : (const char*)p.c.v, in);
+              cp16(ka + r * ROW + swz_k<PIECES>(r, c) * 16, kp + i * RPI * ROW);
+              cp16(va + r * ROW + swz_v<PIECES>(r, c) * 16, vp + i * RPI * ROW);
+            }
+          } else if (c < pieces) {
+#pragma unroll
+            for (int i = 0; i < 16 / RPI; ++i) {
+              const int r = gr + i * RPI + r0;
+              cp16(ka + r * ROW + swz_k<PIECES>(r, c) * 16, kp + i * RPI * row_bytes);
+              cp16(va + r * ROW + swz_v<PIECES>(r, c) * 16, vp + i * RPI * row_bytes);
             }
           }
         }
@@ -291,8 +304,8 @@ __global__ void __launch_bounds__(32 * WARPS, HD <= 128 ? Tile<Q>::CTAS : 1) k_p
           const long long s = __shfl_sync(0xffffffffu, mine, r);
           if (c < pieces) {
             const long long off = s >= 0 ? s + c * 16 : 0;
-            cp16(ka + r * ROW + swz_k<PIECES>(r, c) * 16, (const char*)p.c.k + off, s >= 0);
-            cp16(va + r * ROW + swz_v<PIECES>(r, c) * 16, (const char*)p.c.v + off, s >= 0);
+            cp16_or_zero(ka + r * ROW + swz_k<PIECES>(r, c) * 16, (const char*)p.c.k + off, s >= 0);
+            cp16_or_zero(va + r * ROW + swz_v<PIECES>(r, c) * 16, (const char*)p.c.v + off, s >= 0);
           }
         }
       }
@@ -301,15 +314,16 @@ __global__ void __launch_bounds__(32 * WARPS, HD <= 128 ? Tile<Q>::CTAS : 1) k_p
         ve = __ldg(p.c.ve + slot);
       }
       ist = ist + 1 == STAGES ? 0 : ist + 1;
-      ++ix;
-      if (++it == int_ && ix < w1) {                  // the next group
+      --left;
+      if (++it == int_ && left > 0) {                 // the next group
         it = 0;
-        ix += START;
+        left -= START;
         if (++iseg == segs) {
           iseg = 0;
           do ilen = lens.keys(++ib);
           while (ilen == 0 && ib + 1 < p.B);
           int_ = (ilen + KEYS - 1) / KEYS;
+          table = p.c.table + (long long)ib * p.c.max_pages;
         }
         ig = iseg / n_ht;
       }
@@ -426,7 +440,7 @@ __global__ void __launch_bounds__(32 * WARPS, HD <= 128 ? Tile<Q>::CTAS : 1) k_p
             sc[kg][e] *= Q ? sl2 * __shfl_sync(0xffffffffu, kf, kg * 8 + 2 * j4 + e) : sl2;
             mx = fmaxf(mx, sc[kg][e]);
           }
-        if (ok != (KEYS == 32 ? 0xffffffffu : (1u << KEYS % 32) - 1)) {   // the last tile, or a bad page
+        if (ok != ALL) {                                // the last tile, or a bad page
           mx = -INFINITY;
 #pragma unroll
           for (int kg = 0; kg < NG; ++kg)
@@ -939,6 +953,9 @@ size_t paged_attn_scratch(const PagedView& c) {
 int launch_paged_attn(int dtype, const PagedAttnParams& p0, cudaStream_t s) {
   PagedAttnParams p = p0;
   const bool tc = mma_takes(dtype, p.c);
+  p.ps_shift = -1;
+  for (int i = 0; i < 31; ++i)
+    if (p.c.page_size == 1 << i) p.ps_shift = i;
   const int ctas = tc ? ctas_mma(p.c.e4m3) : ctas_simt();
   p.part_ml = reinterpret_cast<float*>((char*)p.scratch + (size_t)ctas * sizeof(Desc));
   p.part_o = p.part_ml + (size_t)(tc ? ctas * (1 + WARPS) : ctas) * 2 * GT * 2;

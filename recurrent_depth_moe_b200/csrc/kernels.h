@@ -282,6 +282,7 @@ struct PagedAttnParams {
   float scale;
   void* scratch;                                // paged_attn_scratch() bytes
   float* part_o; float* part_ml;
+  int ps_shift;                                 // page_size is 1 << ps_shift, or -1
   DevStatus* st;
 };
 void launch_paged_write(int dtype, const PagedWriteParams& p, cudaStream_t s);

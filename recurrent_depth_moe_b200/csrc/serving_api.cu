@@ -99,6 +99,8 @@ rdt_status rdt_paged_attention(const rdt_paged_cache* cache, int loop, const voi
   const long long w = (long long)n_heads * cache->head_dim;
   if (!q || !o || !lens || q == o || q_ld < w || o_ld < w) return RDT_ERR_INVALID_ARG;
   if (n_heads > 4096 || (long long)batch * n_heads > (1LL << 30)) return RDT_ERR_UNSUPPORTED;
+  // a worker's share of the tiles (16 keys of up to 8 heads, some hundred workers) is counted in 32 bits
+  if ((double)batch * cache->max_pages * cache->page_size * n_heads > 1e12) return RDT_ERR_UNSUPPORTED;
   if (!ws || ((uintptr_t)ws & 255) || ws_bytes < rdt_paged_attention_workspace_size(cache, batch, n_heads))
     return RDT_ERR_WORKSPACE;
   cudaStream_t s = (cudaStream_t)stream;
