@@ -9,10 +9,11 @@
 // order, at which the running sum of the kept weights exceeds u times their total.
 // NaN logits take no part.  T <= 0, or a row with no weight: the most likely token.
 //
-// Weights are rounded to whole numbers of 2^-44, so every sum is exact whatever its order, the
-// same on every run, and a border cannot be missed between two passes.  The exponent
-// (x - m) log2(e) / T is formed in two fp32 words, so a weight is off by about one rounding of
-// its 24 bits wherever it lies.
+// The exponent (x - m) log2(e) / T is formed in two fp32 words, so a weight is off by about one
+// rounding of its 24 bits wherever it lies.  A thread sums its weights in two fp32 words, in a
+// fixed order; beyond a thread weights and sums are whole numbers of 2^-44 in 64 bits, so the
+// result does not depend on the order in which threads arrive.  A sum is off by about 2^-33
+// of itself, a border by as much.
 //
 // A cluster of up to 8 CTAs holds one row in its shared memory, so the logits are read from
 // HBM once; sums, histograms and candidates travel through distributed shared memory and no
@@ -56,8 +57,8 @@ __device__ __forceinline__ u64 place_of(float x, int v) {
 // z = x log2(e) / T as zh + e, in two fp32 words; the weight is 2^(z - M), M that of the maximum.
 struct Weigh {
   float m, chi, clo, nfM, c16;   // log2(e) / T in two words; minus M's fraction; bins per logit
+  float magic;                   // MAGIC minus M's whole part
   float floor;                   // at and below it a weight rounds to nothing
-  int i0;                        // M's whole part (as the bits of i + MAGIC)
   bool wide;                     // |M| so large that z has no fraction left: the difference m - x is formed first
   static constexpr float MAGIC = 12582912.f;   // 1.5 * 2^23: x + MAGIC rounds x to a whole number
   __device__ Weigh(float mx, float T) : m(mx) {
@@ -67,41 +68,51 @@ struct Weigh {
     c16 = fminf(16.f * chi, 3.0e38f);
     const float Mh = mx * chi;
     wide = !(fabsf(Mh) <= 65536.f);
-    const float r = Mh + MAGIC;
-    i0 = __float_as_int(r);
-    nfM = -((Mh - (r - MAGIC)) + (fmaf(mx, chi, -Mh) + mx * clo));
+    const float i0 = (Mh + MAGIC) - MAGIC;
+    magic = MAGIC - i0;
+    nfM = -((Mh - i0) + (fmaf(mx, chi, -Mh) + mx * clo));
     floor = __double2float_rd((double)mx - 32.06 * (double)T);       // 46.25 / log2(e)
   }
   // MAGIC plus the bin, 16 times the exponent rounded to a whole number; monotone in x, NaN for NaN
   __device__ __forceinline__ float bin(float x) const { return fmaf(m - x, c16, MAGIC); }
-  // the weight in units of 2^-44 is q << sh
-  template <bool WIDE> __device__ __forceinline__ void parts(float x, uint32_t& q, int& sh) const {
-    float s;
-    int k;
-    x = fmaxf(x, floor);                                             // also NaN
+  // the weight, to 24 bits (2^-46 for what is below floor, NaN too)
+  template <bool WIDE> __device__ __forceinline__ float weight(float x) const {
+    float s, e;
+    int k;                                                           // minus the whole part of the exponent
+    x = fmaxf(x, floor);
     if (!WIDE) {
-      const float zh = x * chi, r = zh + MAGIC;
-      s = ((zh - (r - MAGIC)) + fmaf(x, clo, nfM)) + fmaf(x, chi, -zh);
-      k = i0 - __float_as_int(r);
+      const float zh = x * chi, r = zh + magic;                      // MAGIC - k
+      s = ((zh - (r - magic)) + fmaf(x, clo, nfM)) + fmaf(x, chi, -zh);
+      k = -__float_as_int(r);                                        // (MAGIC's bits leave the word below)
     } else {
       const float d = m - x, t = d * chi, bb = d - m;
-      const float dlo = (m - (d - bb)) + (-x - bb);                // d + dlo = m - x
+      const float dlo = (m - (d - bb)) + (-x - bb);                  // d + dlo = m - x
       const float r = t + MAGIC;
       s = x == m ? 0.f : -((t - (r - MAGIC)) + (fmaf(d, chi, -t) + fmaf(d, clo, dlo * chi)));
-      k = x == m ? 0 : min(47, __float_as_int(r) - __float_as_int(MAGIC));   // (beyond 47 q is 0)
+      k = x == m ? 0 : min(47, __float_as_int(r) - __float_as_int(MAGIC));
     }
-    const int kk = max(k, 20);
-    sh = kk - k;
-    float e;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(s));            // -1 <= s <= 1
-    q = __float2uint_rn(e * __int_as_float((171 - kk) << 23));       // 2^(44 - kk)
+    return __int_as_float(__float_as_int(e) - (k << 23));
   }
+  // in whole units of 2^-44
   __device__ __forceinline__ u64 operator()(float x) const {
-    uint32_t q;
-    int sh;
-    if (wide) parts<true>(x, q, sh);
-    else parts<false>(x, q, sh);
-    return (u64)q * (u64)(1u << sh);
+    const float w = wide ? weight<true>(x) : weight<false>(x);
+    return w >= 0x1p-45f && bin(x) < MAGIC + BINS ? __float2ull_rn(w * 0x1p44f) : 0;
+  }
+};
+
+// Sum of up to 256 weights of at most 1: `a` stays between 2^8 and 2^9, so a + w rounds w to a
+// multiple of 2^-15 exactly and `lo` takes up what that leaves.
+struct Sum {
+  float a, lo;
+  __device__ __forceinline__ Sum() : a(256.f), lo(0.f) {}
+  __device__ __forceinline__ void add(float w) {
+    const float s = a + w;
+    lo += w - (s - a);
+    a = s;
+  }
+  __device__ __forceinline__ u64 units() const {   // of 2^-44
+    return (u64)__double2ll_rn(((double)(a - 256.f) + (double)lo) * 0x1p44);
   }
 };
 
@@ -560,32 +571,21 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_sample(SampleParams p, int ch
   if (top_p < 1.f) {
     // A weight is counted as 12 bits of 2^-(bin / 16), interpolated linearly in the bin (up to
     // half a bin to each side): off by less than 4e-4 of it, so bins whose running weight is
-    // within 5e-4 of the border bracket it.  All V tokens below (1 - top_p) / V of the largest
-    // weight hold less than 1 - top_p of the total, so the border lies before them: they only
-    // count in the total, which needs no histogram.
+    // within 6e-4 of the border bracket it.  (Tokens below 1e-4 / V of the largest weight hold
+    // less than 1e-4 of the total: they are not counted.)
     const float lim = fminf(MAGIC + (BINS - 1), cut.L);
     const bool cut_any = cut.L < MAGIC + BINS;
-    const float far = MAGIC + fminf((float)BINS, ceilf(16.f * log2f((float)p.vocab / fmaxf(1.f - top_p, 1e-6f))) + 1.f);
-    float tail = 0.f;
+    const float far = fminf(lim, MAGIC + ceilf(16.f * log2f(1e4f * (float)p.vocab)));
+    const uint32_t hist0 = (uint32_t)__cvta_generic_to_shared(sh.hist);
     row.each([&](float x, int l) {
-      const float b = wt.bin(x);
-      if (b <= lim && (!cut_any || cut.holds(b, x, row.index(l)))) {
-        if (b <= far) {
-          const float f = fmaf(wt.m - x, wt.c16, -(b - MAGIC));
-          atomicAdd(&sh.hist[bin_index(b)], __float_as_uint(fmaf(f, -177.45f, 4096.f + 8388608.f)) & 0x3fffu);
-        } else {
-          tail += exp2f((MAGIC - b) * 0.0625f);
-        }
-      }
+      const float b = wt.bin(x), f = fmaf(wt.m - x, wt.c16, MAGIC - b);
+      bool in = b <= far;
+      if (cut_any) in = in && cut.holds(b, x, row.index(l));
+      const uint32_t q = __float_as_uint(fmaf(f, -177.45f, 4096.f + 8388608.f)) & 0x3fffu;
+      asm volatile("{\n .reg .pred p;\n setp.ne.s32 p, %0, 0;\n @p red.shared.add.u32 [%1], %2;\n}" ::"r"((int)in),
+                   "r"(hist0 + 4 * (__float_as_uint(b) - __float_as_uint(MAGIC))), "r"(q) : "memory");
     });
-    tail = warp_sum(tail);
-    if (lane == 0) sh.fred[warp] = tail;
     if (tid < 2) sh.ib[2 + tid] = tid ? BINS - 1 : 0;
-    __syncthreads();
-    if (warp == 0) {
-      tail = warp_sum(lane < NW ? sh.fred[lane] : 0.f);
-      if (lane == 0) sh.mx = tail;
-    }
     cl.sync();
     {
       // the bins in which the running weight reaches the border less, and plus, the margin
@@ -595,9 +595,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_sample(SampleParams p, int ch
 #pragma unroll
       for (int i = 0; i < BPT; ++i) own += w[i] = (u64)((float)c[i] * exp2f(20.f - (float)(BPT * tid + i) / 16.f));
       u64 at = block_scan<NW>(own, sh.red, all) - own;
-      tail = warp_sum(lane < C ? *cl.map_shared_rank(&sh.mx, lane) : 0.f);
-      all += (u64)(tail * 0x1p32f);                              // 2^20 and the 12 bits
-      const u64 b0 = (u64)fmax(0.0, ((double)top_p - 5e-4) * (double)all), b1 = (u64)(((double)top_p + 5e-4) * (double)all);
+      const u64 b0 = (u64)fmax(0.0, ((double)top_p - 6e-4) * (double)all), b1 = (u64)(((double)top_p + 6e-4) * (double)all);
 #pragma unroll
       for (int i = 0; i < BPT; ++i) {
         if (at < b0 && b0 <= at + w[i]) sh.ib[2] = BPT * tid + i;
@@ -607,27 +605,25 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_sample(SampleParams p, int ch
       __syncthreads();
     }
     const float blo = MAGIC + (float)sh.ib[2], bhi = MAGIC + (float)sh.ib[3];
-    u64 total = 0, above = 0;
+    Sum sum_total, sum_above;
     auto weigh = [&](auto wide) {
       sm.list_each4(1, [&](const float* x, int l) {
-        float b[4];
-        uint32_t q[4], bits = 0;
-        int s[4];
+        float b[4], w[4];
+        uint32_t bits = 0;
 #pragma unroll
         for (int e = 0; e < 4; ++e) b[e] = wt.bin(x[e]);
-        if (cut_any && !(b[0] <= lim || b[1] <= lim || b[2] <= lim || b[3] <= lim)) return bits;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) wt.template parts<decltype(wide)::value>(x[e], q[e], s[e]);
         if (cut_any) {
+          if (!(b[0] <= lim || b[1] <= lim || b[2] <= lim || b[3] <= lim)) return bits;
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (!cut.holds(b[e], x[e], row.index(l + e))) q[e] = 0, b[e] = MAGIC + BINS;
+            if (!cut.holds(b[e], x[e], row.index(l + e))) b[e] = MAGIC + BINS;
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const u64 w = (u64)q[e] * (u64)(1u << s[e]);
-          total += w;
-          if (b[e] < blo) above += w;
+          w[e] = wt.template weight<decltype(wide)::value>(x[e]);
+          if (!(b[e] < MAGIC + BINS)) w[e] = 0.f;
+          sum_total.add(w[e]);
+          sum_above.add(b[e] < blo ? w[e] : 0.f);
           if (b[e] >= blo && b[e] <= bhi) bits |= 1u << e;
         }
         return bits;
@@ -635,8 +631,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_sample(SampleParams p, int ch
     };
     if (wt.wide) weigh(std::true_type());
     else weigh(std::false_type());
-    total = warp_sum64(total);
-    above = warp_sum64(above);
+    u64 total = warp_sum64(sum_total.units()), above = warp_sum64(sum_above.units());
     if (lane == 0) sh.wsum[warp] = above, sh.red[warp] = total;
     __syncthreads();
     if (tid == 0) {
@@ -686,29 +681,28 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_sample(SampleParams p, int ch
       if (w) atomicAdd(&sh.wsum[(l >> 2) / piece], w);
     }
   } else {
-    u64 mine = 0;
+    Sum sum;
     auto weigh = [&](auto wide) {
       row.each4([&](const float* x, int l) {
         if (!(x[0] >= xlim || x[1] >= xlim || x[2] >= xlim || x[3] >= xlim)) return;
-        uint32_t q[4];
-        int s[4];
+        float w[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          wt.template parts<decltype(wide)::value>(x[e], q[e], s[e]);
-          if (!(x[e] >= xlim)) q[e] = 0;
+          w[e] = wt.template weight<decltype(wide)::value>(x[e]);
+          if (!(x[e] >= xlim)) w[e] = 0.f;
         }
         if (x[0] == xcut || x[1] == xcut || x[2] == xcut || x[3] == xcut) {
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (drops(x[e], l + e)) q[e] = 0;
+            if (drops(x[e], l + e)) w[e] = 0.f;
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) mine += (u64)q[e] * (u64)(1u << s[e]);
+        for (int e = 0; e < 4; ++e) sum.add(w[e]);
       });
     };
     if (wt.wide) weigh(std::true_type());
     else weigh(std::false_type());
-    mine = warp_sum64(mine);
+    const u64 mine = warp_sum64(sum.units());
     __syncthreads();
     if (lane == 0) sh.wsum[warp] = mine;
   }
@@ -727,6 +721,9 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_sample(SampleParams p, int ch
   __syncthreads();
   if (sh.ib[0] == rank * NW + warp) {
     u64 base = sh.bc[0];
+    int tok = -1;                                                // the last kept token so far
+    float tok_x = 0.f;
+    bool found = false;
     for (int j0 = row.jb; j0 < row.je; j0 += 32) {
       const int j = j0 + lane;
       u64 w[4] = {0, 0, 0, 0};
@@ -745,16 +742,28 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_sample(SampleParams p, int ch
             s += w[e];
             if (s > target) break;
           }
-          const float x = e == 0 ? v.x : e == 1 ? v.y : e == 2 ? v.z : v.w;
-          p.tokens[(long long)r * p.out_ld] = row.index(4 * j + e);
-          if (p.logprob) {
-            const double z = x == mx ? 0.0 : ((double)x - (double)mx) / (double)T;
-            p.logprob[r] = (float)(z - log((double)total * 0x1p-44));
-          }
+          tok_x = e == 0 ? v.x : e == 1 ? v.y : e == 2 ? v.z : v.w;
+          tok = row.index(4 * j + e);
+          found = true;
         }
         break;
       }
+      if (w[0] | w[1] | w[2] | w[3]) {
+        const int e = w[3] ? 3 : w[2] ? 2 : w[1] ? 1 : 0;
+        tok_x = e == 0 ? v.x : e == 1 ? v.y : e == 2 ? v.z : v.w;
+        tok = row.index(4 * j + e);
+      }
       base += __shfl_sync(0xffffffffu, c, 31);
+    }
+    // the warp's sum was off by a rounding and the target lies in it: the last kept token
+    const int top = __reduce_max_sync(0xffffffffu, tok);
+    const bool any = __any_sync(0xffffffffu, found);
+    if (any ? found : tok == top && tok >= 0) {
+      p.tokens[(long long)r * p.out_ld] = tok;
+      if (p.logprob) {
+        const double z = tok_x == mx ? 0.0 : ((double)tok_x - (double)mx) / (double)T;
+        p.logprob[r] = (float)(z - log((double)total * 0x1p-44));
+      }
     }
   }
   cl.barrier_wait();
