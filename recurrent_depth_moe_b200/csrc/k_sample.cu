@@ -54,6 +54,31 @@ __device__ __forceinline__ u64 place_of(float x, int v) {
   return ((u64)key_of(x) << IDX_BITS) | (uint32_t)((1 << IDX_BITS) - 1 - v);
 }
 
+// Two fp32 values handled by one instruction.
+struct F2 {
+  u64 v;
+  __device__ __forceinline__ F2() {}
+  __device__ __forceinline__ F2(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b)); }
+  __device__ __forceinline__ explicit F2(float a) : F2(a, a) {}
+  __device__ __forceinline__ void get(float& a, float& b) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+};
+__device__ __forceinline__ F2 operator+(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ F2 operator-(F2 a, F2 b) { return fma2(b, F2(-1.f), a); }
+
 // z = x log2(e) / T as zh + e, in two fp32 words; the weight is 2^(z - M), M that of the maximum.
 struct Weigh {
   float m, chi, clo, nfM, c16;   // log2(e) / T in two words; minus M's fraction; bins per logit
@@ -94,6 +119,26 @@ struct Weigh {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(s));            // -1 <= s <= 1
     return __int_as_float(__float_as_int(e) - (k << 23));
   }
+  // the same of two
+  template <bool WIDE> __device__ __forceinline__ F2 weight2(float x0, float x1) const {
+    if (WIDE) return F2(weight<true>(x0), weight<true>(x1));
+    const F2 x(fmaxf(x0, floor), fmaxf(x1, floor)), c(chi), mg(magic);
+    const F2 zh = x * c, r = zh + mg;
+    const F2 s = ((zh - (r - mg)) + fma2(x, F2(clo), F2(nfM))) + fma2(x, c, zh * F2(-1.f));
+    float s0, s1, r0, r1, e0, e1;
+    s.get(s0, s1);
+    r.get(r0, r1);
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(s0));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(s1));
+    return F2(__int_as_float(__float_as_int(e0) + (__float_as_int(r0) << 23)),
+              __int_as_float(__float_as_int(e1) + (__float_as_int(r1) << 23)));
+  }
+  // 16 times the exponent of two: MAGIC plus the bins, and by how much it is above them
+  __device__ __forceinline__ void bin2(float x0, float x1, float& b0, float& b1, F2& f) const {
+    const F2 d = F2(m) - F2(x0, x1), c(c16), b = fma2(d, c, F2(MAGIC));
+    f = fma2(d, c, F2(MAGIC) - b);
+    b.get(b0, b1);
+  }
   // in whole units of 2^-44
   __device__ __forceinline__ u64 operator()(float x) const {
     const float w = wide ? weight<true>(x) : weight<false>(x);
@@ -101,18 +146,21 @@ struct Weigh {
   }
 };
 
-// Sum of up to 256 weights of at most 1: `a` stays between 2^8 and 2^9, so a + w rounds w to a
-// multiple of 2^-15 exactly and `lo` takes up what that leaves.
+// Sum of up to 512 weights of at most 1, two at a time: each half of `a` stays between 2^8 and
+// 2^9, so a + w rounds w to a multiple of 2^-15 exactly and `lo` takes up what that leaves.
 struct Sum {
-  float a, lo;
+  F2 a, lo;
   __device__ __forceinline__ Sum() : a(256.f), lo(0.f) {}
-  __device__ __forceinline__ void add(float w) {
-    const float s = a + w;
-    lo += w - (s - a);
+  __device__ __forceinline__ void add(F2 w) {
+    const F2 s = a + w;
+    lo = lo + (w - (s - a));
     a = s;
   }
   __device__ __forceinline__ u64 units() const {   // of 2^-44
-    return (u64)__double2ll_rn(((double)(a - 256.f) + (double)lo) * 0x1p44);
+    float a0, a1, l0, l1;
+    a.get(a0, a1);
+    lo.get(l0, l1);
+    return (u64)__double2ll_rn((((double)a0 + (double)a1 - 512.0) + ((double)l0 + (double)l1)) * 0x1p44);
   }
 };
 
@@ -120,6 +168,7 @@ struct Shared {
   u64 mass[2][RB];
   u64 wsum[NWMAX];       // kept weight of each warp's piece of the row
   u64 glist[2][32];      // [top-k, top-p] the last candidates
+  u64 ranked[32];
   u64 red[NWMAX];
   u64 bc[3];
   u64 total, above;
@@ -127,6 +176,7 @@ struct Shared {
   uint32_t cnt[2][RB];
   uint32_t list[LCAP];
   uint32_t fcnt[2], gcnt[2], kmin[2], kmax[2];
+  uint32_t add[NWMAX][2], nranked;
   uint32_t idx;
   int ib[4];
   float fred[NWMAX];
@@ -376,16 +426,22 @@ template <bool RES, int NT> struct Sampler {
     });
     cl.sync();
     if (threadIdx.x < 32) {
+      // (places are not 0: the unused entries)
       const int lane = threadIdx.x;
-      const int g = lane < C ? min(32, (int)*cl.map_shared_rank(&sh.gcnt[ph], lane)) : 0;
-      int at = lane, from = -1, i = 0;
+      if (lane == 0) sh.nranked = 0;
+      sh.ranked[lane] = 0;
+      u64 got[CMAX];
 #pragma unroll
-      for (int r = 0; r < CMAX; ++r) {
-        const int gr = __shfl_sync(0xffffffffu, g, r);
-        if (at >= 0 && at < gr) from = r, i = at;
-        at -= gr;
-      }
-      const u64 pl = from >= 0 ? cl.map_shared_rank(&sh.glist[ph][0], from)[i] : 0;
+      for (int r = 0; r < CMAX; ++r) got[r] = r < C ? cl.map_shared_rank(&sh.glist[ph][0], r)[lane] : 0;
+      __syncwarp();
+#pragma unroll
+      for (int r = 0; r < CMAX; ++r)
+        if (got[r]) {
+          const uint32_t i = atomicAdd(&sh.nranked, 1u);
+          if (i < 32) sh.ranked[i] = got[r];
+        }
+      __syncwarp();
+      const u64 pl = sh.ranked[lane];
       u64 w = 0, before = base;
       if (pl) w = MASS ? wt(of_key((uint32_t)(pl >> IDX_BITS))) : 1;
 #pragma unroll
@@ -435,6 +491,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_sample(SampleParams p, int ch
   for (int i = tid; i < BINS; i += NT) sh.hist[i] = 0;
   if (tid < 2) sh.fcnt[tid] = sh.gcnt[tid] = sh.kmax[tid] = 0, sh.kmin[tid] = ~0u;
   if (tid == 0) sh.idx = 0x7fffffff;
+  if (tid < 2 * NWMAX) sh.add[tid >> 1][tid & 1] = 0;
+  if (tid < 64) sh.glist[tid >> 5][tid & 31] = 0;
   float mx = -INFINITY;
   if (RES) {                                                     // the whole piece is in flight at once
     const int jf = row.q0 == 0 && row.a ? 1 : 0, jl = (p.vocab + row.a) / 4 - row.q0;   // whole quads: jf .. jl - 1
@@ -576,15 +634,27 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_sample(SampleParams p, int ch
     const float lim = fminf(MAGIC + (BINS - 1), cut.L);
     const bool cut_any = cut.L < MAGIC + BINS;
     const float far = fminf(lim, MAGIC + ceilf(16.f * log2f(1e4f * (float)p.vocab)));
-    const uint32_t hist0 = (uint32_t)__cvta_generic_to_shared(sh.hist);
-    row.each([&](float x, int l) {
-      const float b = wt.bin(x), f = fmaf(wt.m - x, wt.c16, MAGIC - b);
-      bool in = b <= far;
-      if (cut_any) in = in && cut.holds(b, x, row.index(l));
-      const uint32_t q = __float_as_uint(fmaf(f, -177.45f, 4096.f + 8388608.f)) & 0x3fffu;
-      asm volatile("{\n .reg .pred p;\n setp.ne.s32 p, %0, 0;\n @p red.shared.add.u32 [%1], %2;\n}" ::"r"((int)in),
-                   "r"(hist0 + 4 * (__float_as_uint(b) - __float_as_uint(MAGIC))), "r"(q) : "memory");
-    });
+    const uint32_t hist0 = (uint32_t)__cvta_generic_to_shared(sh.hist) - 4 * __float_as_uint(MAGIC);
+    auto count = [&](auto with_cut) {
+      row.each4([&](const float* x, int l) {
+#pragma unroll
+        for (int e = 0; e < 4; e += 2) {
+          float b[2], v[2];
+          F2 f;
+          wt.bin2(x[e], x[e + 1], b[0], b[1], f);
+          fma2(f, F2(-177.45f), F2(4096.f + 8388608.f)).get(v[0], v[1]);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            if (decltype(with_cut)::value && !cut.holds(b[i], x[e + i], row.index(l + e + i))) b[i] = MAGIC + BINS;
+            // (a predicate instead of a branch round each)
+            asm volatile("{\n .reg .pred p;\n setp.le.f32 p, %0, %1;\n @p red.shared.add.u32 [%2], %3;\n}" ::"f"(b[i]),
+                         "f"(far), "r"(hist0 + 4 * __float_as_uint(b[i])), "r"(__float_as_uint(v[i]) & 0x3fffu) : "memory");
+          }
+        }
+      });
+    };
+    if (cut_any) count(std::true_type());
+    else count(std::false_type());
     if (tid < 2) sh.ib[2 + tid] = tid ? BINS - 1 : 0;
     cl.sync();
     {
@@ -606,31 +676,36 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_sample(SampleParams p, int ch
     }
     const float blo = MAGIC + (float)sh.ib[2], bhi = MAGIC + (float)sh.ib[3];
     Sum sum_total, sum_above;
-    auto weigh = [&](auto wide) {
+    auto weigh = [&](auto wide, auto with_cut) {
       sm.list_each4(1, [&](const float* x, int l) {
-        float b[4], w[4];
+        float b[4];
         uint32_t bits = 0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) b[e] = wt.bin(x[e]);
-        if (cut_any) {
+        F2 f;
+        wt.bin2(x[0], x[1], b[0], b[1], f);
+        wt.bin2(x[2], x[3], b[2], b[3], f);
+        if (decltype(with_cut)::value) {
           if (!(b[0] <= lim || b[1] <= lim || b[2] <= lim || b[3] <= lim)) return bits;
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             if (!cut.holds(b[e], x[e], row.index(l + e))) b[e] = MAGIC + BINS;
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          w[e] = wt.template weight<decltype(wide)::value>(x[e]);
-          if (!(b[e] < MAGIC + BINS)) w[e] = 0.f;
-          sum_total.add(w[e]);
-          sum_above.add(b[e] < blo ? w[e] : 0.f);
-          if (b[e] >= blo && b[e] <= bhi) bits |= 1u << e;
+        for (int e = 0; e < 4; e += 2) {
+          float w0, w1;
+          wt.template weight2<decltype(wide)::value>(x[e], x[e + 1]).get(w0, w1);
+          w0 = b[e] < MAGIC + BINS ? w0 : 0.f;
+          w1 = b[e + 1] < MAGIC + BINS ? w1 : 0.f;
+          sum_total.add(F2(w0, w1));
+          sum_above.add(F2(b[e] < blo ? w0 : 0.f, b[e + 1] < blo ? w1 : 0.f));
         }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (b[e] >= blo && b[e] <= bhi) bits |= 1u << e;
         return bits;
       });
     };
-    if (wt.wide) weigh(std::true_type());
-    else weigh(std::false_type());
+    if (wt.wide) cut_any ? weigh(std::true_type(), std::true_type()) : weigh(std::true_type(), std::false_type());
+    else cut_any ? weigh(std::false_type(), std::true_type()) : weigh(std::false_type(), std::false_type());
     u64 total = warp_sum64(sum_total.units()), above = warp_sum64(sum_above.units());
     if (lane == 0) sh.wsum[warp] = above, sh.red[warp] = total;
     __syncthreads();
@@ -655,6 +730,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_sample(SampleParams p, int ch
     if (!ok) {                                                   // the bracket missed the border: the whole order
       cl.sync();
       if (tid == 0) sh.gcnt[1] = 0;
+      if (tid < 32) sh.glist[1][tid] = 0;
       summed = false;
       __syncthreads();
       sm.template resolve<true>(1, true, cut, 0, (1ull << (32 + IDX_BITS)) - 1, (u64)p.vocab, 0, want, place);
@@ -675,11 +751,14 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_sample(SampleParams p, int ch
   auto kept = [&](float x, int l) -> u64 { return x >= xlim && !drops(x, l) ? wt(x) : 0; };
   if (summed && xmin <= xcut) {
     // the weight before the bracket is known: the kept candidates join their pieces
+    // (22 bits to a word: up to LCAP of them fit)
     for (uint32_t i = tid; i < sh.fcnt[1]; i += NT) {
-      const int l = sh.list[i];
-      const u64 w = kept(row.at(l), l);
-      if (w) atomicAdd(&sh.wsum[(l >> 2) / piece], w);
+      const int l = sh.list[i], w = (l >> 2) / piece;
+      const u64 q = kept(row.at(l), l);
+      if (q) atomicAdd(&sh.add[w][0], (uint32_t)q & 0x3fffffu), atomicAdd(&sh.add[w][1], (uint32_t)(q >> 22));
     }
+    __syncthreads();
+    if (tid < NW) sh.wsum[tid] += sh.add[tid][0] + ((u64)sh.add[tid][1] << 22);
   } else {
     Sum sum;
     auto weigh = [&](auto wide) {
@@ -687,9 +766,10 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_sample(SampleParams p, int ch
         if (!(x[0] >= xlim || x[1] >= xlim || x[2] >= xlim || x[3] >= xlim)) return;
         float w[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          w[e] = wt.template weight<decltype(wide)::value>(x[e]);
+        for (int e = 0; e < 4; e += 2) {
+          wt.template weight2<decltype(wide)::value>(x[e], x[e + 1]).get(w[e], w[e + 1]);
           if (!(x[e] >= xlim)) w[e] = 0.f;
+          if (!(x[e + 1] >= xlim)) w[e + 1] = 0.f;
         }
         if (x[0] == xcut || x[1] == xcut || x[2] == xcut || x[3] == xcut) {
 #pragma unroll
@@ -697,7 +777,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_sample(SampleParams p, int ch
             if (drops(x[e], l + e)) w[e] = 0.f;
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sum.add(w[e]);
+        for (int e = 0; e < 4; e += 2) sum.add(F2(w[e], w[e + 1]));
       });
     };
     if (wt.wide) weigh(std::true_type());
