@@ -395,10 +395,37 @@ RDT_API rdt_status rdt_paged_attention(const rdt_paged_cache* cache, int loop, c
                                        const int32_t* lens, int batch, int n_heads, float scale, void* o,
                                        long long o_ld, void* ws, size_t ws_bytes, void* status, void* stream);
 
+/* rdt_recurrent_forward, rdt_recurrent_decode_step(_ex) and rdt_block_forward_cached over a paged
+ * cache (GQA; the cache's dtype, kv heads and head width are the config's).  Keys and values of
+ * the call's rows are written to their pages (positions start_pos + t, or cache_len[b]); a
+ * decode step attends with rdt_paged_attention's kernel; a prefill at start_pos 0 attends to
+ * its own rows as projected, one at start_pos > 0 to positions 0 .. start_pos + seq - 1 read
+ * back from the pages.  cache_len and the table are read on the device.  ws:
+ * rdt_paged_workspace_size bytes for the call's batch, seq and start_pos (0 for a decode step),
+ * used as any other workspace; its first bytes are the call's status word. */
+RDT_API size_t rdt_paged_workspace_size(const rdt_config* cfg, int batch, int seq, int start_pos,
+                                        const rdt_paged_cache* cache);
+RDT_API rdt_status rdt_recurrent_forward_paged(const rdt_config* cfg, const rdt_weights* w, const float* h0,
+                                               const void* e, int batch, int seq, int start_pos, int n_loops,
+                                               float act_threshold, const float* halt_logit_offset, float* h_out,
+                                               float* halt_weights, int32_t* expert_ids,
+                                               const rdt_paged_cache* cache, const rdt_trace* trace, void* ws,
+                                               size_t ws_bytes, void* stream);
+RDT_API rdt_status rdt_recurrent_decode_step_paged(const rdt_config* cfg, const rdt_weights* w, const float* h0,
+                                                   const void* e, int batch, const int32_t* cache_len, int n_loops,
+                                                   float act_threshold, const float* halt_logit_offset,
+                                                   float* h_out, float* halt_weights, int32_t* expert_ids,
+                                                   const rdt_paged_cache* cache, const rdt_trace* trace, void* ws,
+                                                   size_t ws_bytes, void* stream);
+RDT_API rdt_status rdt_block_forward_paged(const rdt_config* cfg, const rdt_weights* w, const float* x_in,
+                                           float* x_out, int batch, int seq, int start_pos,
+                                           const int32_t* cache_len, const rdt_paged_cache* cache, void* ws,
+                                           size_t ws_bytes, void* stream);
+
 /* ---- sampled next token -------------------------------------------------------------------
  * The generation loop is printed without a sampling rule; rdt_greedy_tokens is its plainest
  * reading, and this is the usual one.  Per row of logits x with maximum m and temperature T,
- * token v weighs w_v = exp((x_v - m) / T), rounded to multiples of 2^-44.  In the order of the logits,
+ * token v weighs w_v = exp((x_v - m) / T) (below 2^-45: nothing).  In the order of the logits,
  * ties by the lower index: top_k > 0 keeps the first top_k tokens; top_p < 1 keeps, of these,
  * the tokens whose preceding tokens hold less than top_p of their weight; min_p > 0 keeps, of
  * these, those with w_v >= min_p.  The first token of the order always stays.  The result is

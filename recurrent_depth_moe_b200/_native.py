@@ -84,7 +84,8 @@ EXPORTS = ("rdt_workspace_size", "rdt_recurrent_forward", "rdt_recurrent_decode_
            "rdt_depth_batch_workspace_size", "rdt_depth_batch_begin", "rdt_depth_batch_tick",
            "rdt_depth_batch_pending", "rdt_depth_batch_run",
            "rdt_paged_kv_write", "rdt_paged_kv_read", "rdt_paged_attention_workspace_size", "rdt_paged_attention",
-           "rdt_sample_tokens")
+           "rdt_sample_tokens", "rdt_paged_workspace_size", "rdt_recurrent_forward_paged",
+           "rdt_recurrent_decode_step_paged", "rdt_block_forward_paged")
 
 _lib = None
 _profiling = False
@@ -147,7 +148,16 @@ def load(path: str = LIB_PATH):
     lib.rdt_paged_attention.argtypes = [C, c_int, P, ctypes.c_longlong, P, c_int, c_int, c_float, P,
                                         ctypes.c_longlong, P, c_size_t, P, P]
     lib.rdt_sample_tokens.argtypes = [P, ctypes.c_longlong, c_int, c_int, P, POINTER(rdt_sampling), P, c_int, P, P]
-    for fn in ("rdt_paged_kv_write", "rdt_paged_kv_read", "rdt_paged_attention", "rdt_sample_tokens"):
+    lib.rdt_paged_workspace_size.argtypes = [POINTER(rdt_config), c_int, c_int, c_int, C]
+    lib.rdt_paged_workspace_size.restype = c_size_t
+    lib.rdt_recurrent_forward_paged.argtypes = [POINTER(rdt_config), POINTER(rdt_weights), P, P, c_int, c_int, c_int,
+                                                c_int, c_float, P, P, P, P, C, POINTER(rdt_trace), P, c_size_t, P]
+    lib.rdt_recurrent_decode_step_paged.argtypes = [POINTER(rdt_config), POINTER(rdt_weights), P, P, c_int, P, c_int,
+                                                    c_float, P, P, P, P, C, POINTER(rdt_trace), P, c_size_t, P]
+    lib.rdt_block_forward_paged.argtypes = [POINTER(rdt_config), POINTER(rdt_weights), P, P, c_int, c_int, c_int, P, C,
+                                            P, c_size_t, P]
+    for fn in ("rdt_recurrent_forward_paged", "rdt_recurrent_decode_step_paged", "rdt_block_forward_paged",
+               "rdt_paged_kv_write", "rdt_paged_kv_read", "rdt_paged_attention", "rdt_sample_tokens"):
         getattr(lib, fn).restype = c_int
     lib.rdt_read_device_status.argtypes = [P, P]
     lib.rdt_read_device_status.restype = c_int

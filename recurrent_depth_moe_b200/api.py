@@ -9,11 +9,12 @@ from __future__ import annotations
 
 import ctypes
 from dataclasses import dataclass
-from typing import Optional
+from typing import Optional, Union
 
 import torch
 
 from . import _native as N
+from .serving import PagedKVCache, sample_tokens
 
 _DT = {"fp32": (0, torch.float32), "bf16": (1, torch.bfloat16)}
 
@@ -118,6 +119,11 @@ def workspace_size(cfg_struct: N.rdt_config, batch: int, seq: int, max_keys: int
     return int(lib.rdt_workspace_size(ctypes.byref(cfg_struct), batch, seq, max_keys))
 
 
+def paged_workspace_size(cfg_struct: N.rdt_config, batch: int, seq: int, start_pos: int, cache: PagedKVCache) -> int:
+    return int(N.load().rdt_paged_workspace_size(ctypes.byref(cfg_struct), batch, seq, start_pos,
+                                                 ctypes.byref(cache.struct())))
+
+
 def alloc_workspace(nbytes: int, device=None) -> torch.Tensor:
     """Workspace as a torch uint8 buffer (torch's allocator returns >= 512-byte aligned blocks)."""
     ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device or "cuda")
@@ -182,19 +188,21 @@ class RecurrentBlock:
         self.w = Weights(weights, self.dtype)
         self._ws = None
 
-    def workspace(self, batch: int, seq: int, max_keys: int) -> torch.Tensor:
-        need = workspace_size(self.cs, batch, seq, max_keys)
+    def workspace(self, batch: int, seq: int, max_keys: int, start_pos: int = 0,
+                  cache: Optional[PagedKVCache] = None) -> torch.Tensor:
+        need = workspace_size(self.cs, batch, seq, max_keys) if cache is None else \
+            paged_workspace_size(self.cs, batch, seq, start_pos, cache)
         if need == 0:
-            raise N.RdtError("rdt_workspace_size", N.RDT_ERR_INVALID_ARG)
+            raise N.RdtError("rdt_workspace_size" if cache is None else "rdt_paged_workspace_size", N.RDT_ERR_INVALID_ARG)
         if self._ws is None or self._ws.numel() < need:
             self._ws = alloc_workspace(need)
         return self._ws
 
     def forward(self, h0: torch.Tensor, e: torch.Tensor, batch: int, seq: int, n_loops: int,
                 act_threshold: float = 0.0, start_pos: int = 0, halt_logit_offset: Optional[torch.Tensor] = None,
-                cache: Optional[KVCache] = None, trace: Optional[Trace] = None, flags: int = 0,
+                cache: Union[KVCache, PagedKVCache, None] = None, trace: Optional[Trace] = None, flags: int = 0,
                 out: Optional[tuple] = None, workspace: Optional[torch.Tensor] = None):
-        """rdt_recurrent_forward.  Returns (h_out [N, D] fp32, halt_weights [L, N] fp32,
+        """rdt_recurrent_forward (rdt_recurrent_forward_paged over a paged cache).  Returns (h_out [N, D] fp32, halt_weights [L, N] fp32,
         expert_ids [L, N, k] int32)."""
         lib = N.load()
         cfg = self.cfg
@@ -208,9 +216,21 @@ class RecurrentBlock:
                    torch.empty(n_loops, Nr, dtype=torch.float32, device=h0.device),
                    torch.empty(n_loops, Nr, cfg.n_experts_per_tok, dtype=torch.int32, device=h0.device))
         max_keys = start_pos + seq if cache is None else max(start_pos + seq, cache.t_max)
+        ts = trace.struct() if trace is not None else None
+        if isinstance(cache, PagedKVCache):
+            if flags:
+                raise ValueError("flags: not with a paged cache")
+            ws = workspace if workspace is not None else self.workspace(batch, seq, max_keys, start_pos, cache)
+            rc = lib.rdt_recurrent_forward_paged(ctypes.byref(self.cs), ctypes.byref(self.w.struct), h0.data_ptr(),
+                                                 e.data_ptr(), batch, seq, start_pos, n_loops, float(act_threshold),
+                                                 _ptr(halt_logit_offset), out[0].data_ptr(), out[1].data_ptr(),
+                                                 out[2].data_ptr(), ctypes.byref(cache.struct()),
+                                                 ctypes.byref(ts) if ts is not None else None, ws.data_ptr(),
+                                                 ws.numel(), _stream())
+            N.check("rdt_recurrent_forward_paged", rc)
+            return out
         ws = workspace if workspace is not None else self.workspace(batch, seq, max_keys)
         cs = cache.struct() if cache is not None else None
-        ts = trace.struct() if trace is not None else None
         rc = lib.rdt_recurrent_forward(ctypes.byref(self.cs), ctypes.byref(self.w.struct), h0.data_ptr(),
                                        e.data_ptr(), batch, seq, start_pos, n_loops, float(act_threshold),
                                        _ptr(halt_logit_offset), out[0].data_ptr(), out[1].data_ptr(),
@@ -220,12 +240,13 @@ class RecurrentBlock:
         N.check("rdt_recurrent_forward", rc)
         return out
 
-    def decode_step(self, h0: torch.Tensor, e: torch.Tensor, cache_len: torch.Tensor, cache: KVCache,
+    def decode_step(self, h0: torch.Tensor, e: torch.Tensor, cache_len: torch.Tensor, cache: Union[KVCache, PagedKVCache],
                     n_loops: int, act_threshold: float = 0.0, out: Optional[tuple] = None,
                     workspace: Optional[torch.Tensor] = None, trace: Optional[Trace] = None,
                     halt_logit_offset: Optional[torch.Tensor] = None):
         """rdt_recurrent_decode_step: one new token per sequence at position cache_len[b]
-        (rdt_recurrent_decode_step_ex when a trace or halting-logit offsets are given)."""
+        (rdt_recurrent_decode_step_ex when a trace or halting-logit offsets are given,
+        rdt_recurrent_decode_step_paged over a paged cache)."""
         lib = N.load()
         cfg = self.cfg
         B = h0.shape[0]
@@ -236,8 +257,21 @@ class RecurrentBlock:
             out = (torch.empty(B, cfg.dim, dtype=torch.float32, device=h0.device),
                    torch.empty(n_loops, B, dtype=torch.float32, device=h0.device),
                    torch.empty(n_loops, B, cfg.n_experts_per_tok, dtype=torch.int32, device=h0.device))
-        ws = workspace if workspace is not None else self.workspace(B, 1, cache.t_max)
+        paged = isinstance(cache, PagedKVCache)
+        ws = workspace if workspace is not None else self.workspace(B, 1, cache.t_max, cache=cache if paged else None)
         cs = cache.struct()
+        if paged:
+            if halt_logit_offset is not None:
+                _check_act(halt_logit_offset, "halt_logit_offset", torch.float32, (B,))
+            ts = trace.struct() if trace is not None else None
+            rc = lib.rdt_recurrent_decode_step_paged(ctypes.byref(self.cs), ctypes.byref(self.w.struct), h0.data_ptr(),
+                                                     e.data_ptr(), B, cache_len.data_ptr(), n_loops,
+                                                     float(act_threshold), _ptr(halt_logit_offset), out[0].data_ptr(),
+                                                     out[1].data_ptr(), out[2].data_ptr(), ctypes.byref(cs),
+                                                     ctypes.byref(ts) if ts is not None else None, ws.data_ptr(),
+                                                     ws.numel(), _stream())
+            N.check("rdt_recurrent_decode_step_paged", rc)
+            return out
         if trace is not None or halt_logit_offset is not None:
             if halt_logit_offset is not None:
                 _check_act(halt_logit_offset, "halt_logit_offset", torch.float32, (B,))
@@ -272,13 +306,14 @@ class DecodeGraph:
     replays it, every later call replays.  Calls made while the library's profiler records
     run eagerly, since its CUDA events are recorded at launch time."""
 
-    def __init__(self, blk: "RecurrentBlock", batch: int, cache: KVCache, cache_len: torch.Tensor, n_loops: int,
+    def __init__(self, blk: "RecurrentBlock", batch: int, cache: Union[KVCache, PagedKVCache], cache_len: torch.Tensor, n_loops: int,
                  act_threshold: float = 0.0, workspace: Optional[torch.Tensor] = None, out: Optional[tuple] = None,
                  halt_logit_offset: bool = False):
         cfg = blk.cfg
         self.blk, self.B, self.cache, self.cache_len = blk, batch, cache, cache_len
         self.L, self.thr = n_loops, act_threshold
-        self.ws = workspace if workspace is not None else blk.workspace(batch, 1, cache.t_max)
+        self.ws = workspace if workspace is not None else blk.workspace(
+            batch, 1, cache.t_max, cache=cache if isinstance(cache, PagedKVCache) else None)
         self.out = out if out is not None else (
             torch.empty(batch, cfg.dim, dtype=torch.float32, device="cuda"),
             torch.empty(n_loops, batch, dtype=torch.float32, device="cuda"),
@@ -423,20 +458,36 @@ class Block:
             self.cs = config_struct(cfg)
         self.w = Weights(weights, _DT[cfg.dtype][1])
 
-    def workspace(self, batch: int, seq: int, max_keys: int) -> torch.Tensor:
-        return alloc_workspace(workspace_size(self.cs, batch, seq, max_keys))
+    def workspace(self, batch: int, seq: int, max_keys: int, start_pos: int = 0,
+                  cache: Optional[PagedKVCache] = None) -> torch.Tensor:
+        if cache is None:
+            return alloc_workspace(workspace_size(self.cs, batch, seq, max_keys))
+        need = paged_workspace_size(self.cs, batch, seq, start_pos, cache)
+        if need == 0:
+            raise N.RdtError("rdt_paged_workspace_size", N.RDT_ERR_INVALID_ARG)
+        return alloc_workspace(need)
 
-    def forward(self, x: torch.Tensor, batch: int, seq: int, start_pos: int = 0, cache: Optional[KVCache] = None,
+    def forward(self, x: torch.Tensor, batch: int, seq: int, start_pos: int = 0,
+                cache: Union[KVCache, PagedKVCache, None] = None,
                 cache_len: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
                 workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
         """rdt_block_forward_cached: prefill at start_pos (cache_len None) or one decode
-        step at positions cache_len[b] (seq 1); cache None = no cache."""
+        step at positions cache_len[b] (seq 1); cache None = no cache.  Over a paged cache:
+        rdt_block_forward_paged."""
         lib = N.load()
         _check_act(x, "x", torch.float32, (batch * seq, self.cfg.dim))
         if cache_len is not None:
             _check_act(cache_len, "cache_len", torch.int32, (batch,))
         out = torch.empty_like(x) if out is None else out
         max_keys = start_pos + seq if cache is None else max(start_pos + seq, cache.t_max)
+        if isinstance(cache, PagedKVCache):
+            ws = workspace if workspace is not None else self.workspace(batch, seq, max_keys, start_pos, cache)
+            rc = lib.rdt_block_forward_paged(ctypes.byref(self.cs), ctypes.byref(self.w.struct), x.data_ptr(),
+                                             out.data_ptr(), batch, seq, start_pos,
+                                             None if cache_len is None else cache_len.data_ptr(),
+                                             ctypes.byref(cache.struct()), ws.data_ptr(), ws.numel(), _stream())
+            N.check("rdt_block_forward_paged", rc)
+            return out
         ws = workspace if workspace is not None else self.workspace(batch, seq, max_keys)
         cs = cache.struct() if cache is not None else None
         rc = lib.rdt_block_forward_cached(ctypes.byref(self.cs), ctypes.byref(self.w.struct), x.data_ptr(),
@@ -551,13 +602,25 @@ def _layer_cache(cfg, n_loops: int, batch: int, t_max: int) -> KVCache:
                    torch.zeros(n_loops, batch, t_max, cfg.qk_rope_head_dim, dtype=dt, device="cuda"))
 
 
+@dataclass
+class Sampling:
+    """How a Generator draws its tokens (sample_tokens): numbers for every sequence, or tensors
+    with one per sequence (fp32 [batch]; top_k int32)."""
+    temperature: Union[float, torch.Tensor] = 1.0
+    top_k: Union[int, torch.Tensor] = 0
+    top_p: Union[float, torch.Tensor] = 1.0
+    min_p: Union[float, torch.Tensor] = 0.0
+
+
 class Generator:
     """OpenMythos.generate on the library's entry points ("OpenMythos 분석", RoPE &
     generation cache): step 0 runs the whole prompt at start_pos 0 and fills one cache per
     prelude / coda layer and per recurrent loop; every later step runs the last token
     alone at position prompt_len + step - 1 against those caches.  The next token is the
-    greedy choice (rdt_greedy_tokens).  All buffers are allocated once per generator, so
-    the decode steps allocate nothing.
+    greedy choice (rdt_greedy_tokens) or, with `sampling`, drawn with the uniform numbers
+    `u` [max_new_tokens, batch] of run() (rdt_sample_tokens).  With page_size the caches are
+    paged (GQA), quantised to e4m3 as they are written with `quantised`.  All buffers are
+    allocated once per generator, so the decode steps allocate nothing.
 
     With cuda_graph (the default) the decode step's launches (about 20 per loop plus the
     prelude, coda, head and greedy choice) are captured once into a CUDA graph on the
@@ -568,8 +631,14 @@ class Generator:
     call made while the library's profiler is recording."""
 
     def __init__(self, cfg, MW: dict, batch: int, prompt_len: int, max_new_tokens: int, n_loops: int,
-                 act_threshold: float = 0.0, cuda_graph: bool = True, trace: bool = False):
+                 act_threshold: float = 0.0, cuda_graph: bool = True, trace: bool = False,
+                 sampling: Optional[Sampling] = None, page_size: Optional[int] = None, quantised: bool = False):
         _require_cuda()
+        if quantised and page_size is None:
+            raise ValueError("quantised: needs a paged cache (page_size)")
+        self.sampling = sampling
+        self.u = torch.zeros(max_new_tokens, batch, dtype=torch.float32, device="cuda")
+        self.u_in = torch.zeros(batch, dtype=torch.float32, device="cuda")      # of the step in hand
         self.cfg, self.MW = cfg, MW
         self.B, self.T0, self.new, self.L, self.thr = batch, prompt_len, max_new_tokens, n_loops, act_threshold
         self.t_max = prompt_len + max_new_tokens
@@ -577,13 +646,20 @@ class Generator:
         self.pre = [Block(cfg, W) for W in MW["prelude"]]
         self.coda = [Block(cfg, W) for W in MW["coda"]]
         self.rb = RecurrentBlock(cfg, MW["recurrent"])
-        self.pre_cache = [_layer_cache(cfg, 1, B, self.t_max) for _ in self.pre]
-        self.coda_cache = [_layer_cache(cfg, 1, B, self.t_max) for _ in self.coda]
-        self.rec_cache = _layer_cache(cfg, n_loops, B, self.t_max)
-        sizes = [workspace_size(b.cs, B, s, self.t_max) for b in self.pre + self.coda for s in (T0, 1)]
+        if page_size is None:
+            make = lambda loops: _layer_cache(cfg, loops, B, self.t_max)
+            size = lambda cs, s, cache: workspace_size(cs, B, s, self.t_max)
+        else:
+            make = lambda loops: PagedKVCache.alloc(cfg, loops, B, self.t_max, page_size, quantised)
+            size = lambda cs, s, cache: paged_workspace_size(cs, B, s, 0, cache)
+        self.pre_cache = [make(1) for _ in self.pre]
+        self.coda_cache = [make(1) for _ in self.coda]
+        self.rec_cache = make(n_loops)
+        sizes = [size(b.cs, s, c) for b, c in zip(self.pre + self.coda, self.pre_cache + self.coda_cache) for s in (T0, 1)]
         self.ws_block = alloc_workspace(max(sizes + [256]))
-        self.ws_rec_prefill = self.rb.workspace(B, T0, self.t_max)
-        self.ws_rec_decode = self.rb.workspace(B, 1, self.t_max)
+        paged = self.rec_cache if page_size is not None else None
+        self.ws_rec_prefill = self.rb.workspace(B, T0, self.t_max, cache=paged)
+        self.ws_rec_decode = self.rb.workspace(B, 1, self.t_max, cache=paged)
         cs = config_struct(cfg)
         self.ws_head = alloc_workspace(workspace_size(cs, 1, B, B))
         V = MW["head"].shape[0]
@@ -633,11 +709,20 @@ class Generator:
                         workspace=self.ws_rec_prefill, trace=self.trace_prefill)
         x, y = self._run_blocks(self.coda, self.coda_cache, self.rec_out[0], y, T0, 0, None)
         head(self.cfg, x, self.MW["norm_w"], self.MW["head"], last_of=T0, out=self.logits, workspace=self.ws_head)
-        greedy_tokens(self.logits, out=self.tokens[0])
+        self.u_in.copy_(self.u[0])
+        self._choose(self.tokens[0])
         return self.tokens[0]
 
+    def _choose(self, tok_out: torch.Tensor):
+        """The next tokens from self.logits (and the uniform numbers in self.u_in)."""
+        if self.sampling is None:
+            greedy_tokens(self.logits, out=tok_out)
+        else:
+            s = self.sampling
+            sample_tokens(self.logits, self.u_in, s.temperature, s.top_k, s.top_p, s.min_p, out=tok_out)
+
     def _decode_body(self, tok_in: torch.Tensor, tok_out: torch.Tensor):
-        """One decode step from the tokens in tok_in [B] to the greedy tokens in tok_out [B],
+        """One decode step from the tokens in tok_in [B] to the next tokens in tok_out [B],
         with the cache length already in self.cache_len."""
         B = self.B
         lib = N.load()
@@ -653,11 +738,12 @@ class Generator:
                             workspace=self.ws_rec_decode, trace=self.trace_decode)
         x, y = self._run_blocks(self.coda, self.coda_cache, out[0], y, 1, 0, self.cache_len)
         head(self.cfg, x, self.MW["norm_w"], self.MW["head"], out=self.logits, workspace=self.ws_head)
-        greedy_tokens(self.logits, out=tok_out)
+        self._choose(tok_out)
 
     def decode(self, step: int) -> torch.Tensor:
         """Step `step` >= 1: the token of step - 1 at position prompt_len + step - 1."""
         self.cache_len.fill_(self.T0 + step - 1)
+        self.u_in.copy_(self.u[step])
         if not self.cuda_graph or N.profiling() or self._eager_decodes == 0:
             self._decode_body(self.tokens[step - 1], self.tokens[step])
             self._eager_decodes += 1
@@ -676,8 +762,14 @@ class Generator:
         self.tokens[step].copy_(self.cur_tok)
         return self.tokens[step]
 
-    def run(self, prompt_ids: torch.Tensor) -> torch.Tensor:
-        """Prompt [B, T0] -> the generated tokens [B, max_new_tokens] (int32, CUDA)."""
+    def run(self, prompt_ids: torch.Tensor, u: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """Prompt [B, T0] -> the generated tokens [B, max_new_tokens] (int32, CUDA).  u: uniform
+        numbers in [0, 1) [max_new_tokens, B] for the sampled tokens (needed with `sampling`)."""
+        if (u is None) != (self.sampling is None):
+            raise ValueError("u must be given exactly when the generator samples")
+        if u is not None:
+            _check_act(u, "u", torch.float32, (self.new, self.B))
+            self.u.copy_(u)
         self.prefill(prompt_ids)
         for step in range(1, self.new):
             self.decode(step)
@@ -685,10 +777,14 @@ class Generator:
 
 
 def generate(cfg, MW: dict, prompt_ids: torch.Tensor, max_new_tokens: int, n_loops: int,
-             act_threshold: float = 0.0) -> torch.Tensor:
-    """Greedy generation: returns [B, T0 + max_new_tokens] token ids (int32, CUDA)."""
+             act_threshold: float = 0.0, sampling: Optional[Sampling] = None, u: Optional[torch.Tensor] = None,
+             page_size: Optional[int] = None, quantised: bool = False) -> torch.Tensor:
+    """Generation, greedy or with `sampling` from the uniform numbers u [max_new_tokens, B], over
+    contiguous or (page_size) paged caches: returns [B, T0 + max_new_tokens] token ids (int32,
+    CUDA)."""
     B, T0 = prompt_ids.shape
     ids = prompt_ids.to(device="cuda", dtype=torch.int32).contiguous()
-    gen = Generator(cfg, MW, B, T0, max_new_tokens, n_loops, act_threshold)
-    new = gen.run(ids)
+    gen = Generator(cfg, MW, B, T0, max_new_tokens, n_loops, act_threshold, sampling=sampling, page_size=page_size,
+                    quantised=quantised)
+    new = gen.run(ids, u)
     return torch.cat([ids, new], dim=1)

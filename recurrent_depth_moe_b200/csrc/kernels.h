@@ -268,7 +268,7 @@ struct PagedWriteParams {
 };
 struct PagedReadParams {
   PagedView c;
-  const int* lens; int len_add;                 // positions 0 .. lens[b] + len_add - 1
+  const int* lens; int len_add;                 // positions 0 .. lens[b] (0 without lens) + len_add - 1
   int B, t_out;
   void* k_out; void* v_out;                     // [B][Hkv][t_out][hd] model dtype
   DevStatus* st;

@@ -66,10 +66,10 @@ __device__ __forceinline__ int page_of(const PagedView& c, int b, int pos, DevSt
   return page;
 }
 
-// Visible keys of sequence b: its length plus len_add, inside what its table can hold.
+// Visible keys of sequence b: its length (0 without lens) plus len_add, inside what its table can hold.
 __device__ __forceinline__ int visible_keys(const PagedView& c, const int* lens, int b, int len_add, DevStatus* st,
                                             int where) {
-  const int n = __ldg(lens + b) + len_add;
+  const int n = (lens ? __ldg(lens + b) : 0) + len_add;
   const long long cap = (long long)c.max_pages * c.page_size;
   if (n > cap) {
     record_status(st, ST_BOUNDS, where, n);

@@ -5,6 +5,7 @@
 #include "../../include/rdt.h"
 #include "common.cuh"
 #include "kernels.h"
+#include "paged_host.h"
 
 #include <string.h>
 #include <algorithm>
@@ -168,7 +169,27 @@ struct Ctx {
   bool compact_q = false;          // prefill with ACT: attention queries and O projection on the running rows
   bool test_mla_timeout = false;   // test only: RDT_FLAG_TEST_MLA_ATTN_TIMEOUT
   bool test_mla_done = false;      // ... and its attention was launched
+  const rdt_paged_cache* paged = nullptr;   // GQA keys / values in pages instead of a rdt_kv_cache
+  size_t paged_off = 0;                     // its part of the workspace, behind the layout
 };
+
+// What a paged cache needs behind the layout: the decode attention's parts, or for a prefill
+// behind cached positions those positions read back, K then V [B][Hkv][start_pos + T][hd].
+size_t paged_ws_bytes(const rdt_config* c, const rdt_paged_cache* pc, int B, int T, int start_pos, bool decode) {
+  if (decode) return align256(paged_attn_scratch(paged_view(pc, 0)));
+  if (start_pos == 0) return 0;
+  return 2 * align256((size_t)B * c->n_kv_heads * (start_pos + T) * (c->dim / c->n_heads) * esize(c));
+}
+rdt_status check_paged(const rdt_config* c, const rdt_paged_cache* pc, int B, int T, int start_pos, int n_loops) {
+  rdt_status st = check_paged_cache(pc);
+  if (st != RDT_OK) return st;
+  if (c->attn_type != 0) return RDT_ERR_UNSUPPORTED;
+  if (pc->dtype != c->dtype || pc->n_kv_heads != c->n_kv_heads || pc->head_dim != c->dim / c->n_heads ||
+      pc->batch < B || pc->n_loops < n_loops || start_pos + (long long)T > (long long)pc->max_pages * pc->page_size)
+    return RDT_ERR_INVALID_ARG;
+  if ((long long)B * T * pc->n_kv_heads > (1LL << 31)) return RDT_ERR_UNSUPPORTED;
+  return RDT_OK;
+}
 
 #define RDT_TRY(x)                          \
   do {                                      \
@@ -201,7 +222,7 @@ rdt_status attention_block(Ctx& x, int B, int T, const float* combined, const vo
   memset(&ap, 0, sizeof(ap));
   ap.B = B; ap.T = T; ap.H = H; ap.q_pos = pos; ap.st = x.st;
   int dv;
-  bool absorbed = false;   // MLA decode ran in the absorbed form (attention output written)
+  bool absorbed = false;   // the attention output is written (MLA decode in the absorbed form, paged decode)
   if (c->attn_type == 0) {
     const int Hkv = c->n_kv_heads, hd = D / H, W = (H + 2 * Hkv) * hd;
     void* qkv = at<void*>(x.ws, x.L.qkv);
@@ -211,7 +232,7 @@ rdt_status attention_block(Ctx& x, int B, int T, const float* combined, const vo
     g.rope[0] = RopeDesc{0, H, hd, 0, hd};
     g.rope[1] = RopeDesc{H * hd, Hkv, hd, 0, hd};
     // the tensor-core attention reads V transposed; the QKV epilogue writes that copy
-    const bool kv_from_qkv = !(cache && cache->k && (decode || start_pos > 0));
+    const bool kv_from_qkv = !((x.paged || (cache && cache->k)) && (decode || start_pos > 0));
     bool want_vt = x.dtype == 1 && hd == 128 && T % 8 == 0 && kv_from_qkv && !decode;
     if (want_vt) {
       g.vt = at<void*>(x.ws, x.L.vt); g.vt_col0 = (H + Hkv) * hd; g.vt_heads = Hkv; g.vt_hd = hd; g.vt_T = T; g.vt_ld = T;
@@ -259,6 +280,45 @@ rdt_status attention_block(Ctx& x, int B, int T, const float* combined, const vo
     ap.q_head = hd; ap.dn = hd; ap.dr = 0; ap.dv = hd; ap.G = H / Hkv;
     ap.scale = 1.f / sqrtf((float)hd);
     const bool use_cache = cache && cache->k;
+    if (x.paged) {
+      {
+        ProfScope ps(PC_OTHER, x.s);
+        PagedWriteParams pw;
+        memset(&pw, 0, sizeof(pw));
+        pw.c = paged_view(x.paged, loop_t);
+        pw.k = (const char*)qkv + (size_t)H * hd * es; pw.v = (const char*)qkv + (size_t)(H + Hkv) * hd * es; pw.ld = W;
+        pw.pos = pos; pw.n_rows = N; pw.seq = T; pw.st = x.st;
+        launch_paged_write(x.dtype, pw, x.s);
+      }
+      if (decode) {
+        PagedAttnParams pa;
+        memset(&pa, 0, sizeof(pa));
+        pa.c = paged_view(x.paged, loop_t);
+        pa.q = qkv; pa.q_row = W; pa.o = attn; pa.o_row = (long long)H * hd;
+        pa.lens = pos; pa.len_add = 1;      // the new token's own position included
+        pa.B = B; pa.H = H; pa.scale = ap.scale; pa.scratch = at<void*>(x.ws, x.paged_off); pa.st = x.st;
+        ProfScope ps(PC_ATTN, x.s);
+        RDT_TRY(launch_paged_attn(x.dtype, pa, x.s));
+        absorbed = true;
+      } else if (start_pos > 0) {
+        const int keys = start_pos + T;
+        PagedReadParams pr;
+        memset(&pr, 0, sizeof(pr));
+        pr.c = paged_view(x.paged, loop_t);
+        pr.len_add = keys; pr.B = B; pr.t_out = keys;
+        pr.k_out = at<void*>(x.ws, x.paged_off);
+        pr.v_out = (char*)pr.k_out + align256((size_t)B * Hkv * keys * hd * es);
+        pr.st = x.st;
+        {
+          ProfScope ps(PC_OTHER, x.s);
+          launch_paged_read(x.dtype, pr, x.s);
+        }
+        const long long sj = hd, sg = (long long)keys * hd, sb = (long long)Hkv * sg;
+        ap.k1 = pr.k_out; ap.k1_b = sb; ap.k1_j = sj; ap.k1_g = sg;
+        ap.v = pr.v_out; ap.v_b = sb; ap.v_j = sj; ap.v_g = sg;
+        ap.key_pos0 = 0; ap.n_keys = keys;
+      }
+    }
     if (use_cache) {
       const long long loop_elems = (long long)cache->batch * Hkv * cache->t_max * hd;
       size_t per_loop = (size_t)loop_elems * es;
@@ -496,7 +556,8 @@ rdt_status check_ws(void* ws, size_t ws_bytes, const Layout& L) {
 rdt_status run_recurrent(const rdt_config* c, const rdt_weights* w, const float* h0, const void* e, int B, int T,
                          int start_pos, const int32_t* cache_len, int n_loops, float thr, const float* halt_off,
                          float* h_out, float* halt_weights, int32_t* expert_ids, const rdt_kv_cache* cache,
-                         const rdt_trace* trace, int flags, void* ws, size_t ws_bytes, cudaStream_t s, bool decode) {
+                         const rdt_trace* trace, int flags, void* ws, size_t ws_bytes, cudaStream_t s, bool decode,
+                         const rdt_paged_cache* paged = nullptr) {
   rdt_status st = check_config(c);
   if (st != RDT_OK) return st;
   if ((st = check_block_weights(c, w, true)) != RDT_OK) return st;
@@ -515,15 +576,22 @@ rdt_status run_recurrent(const rdt_config* c, const rdt_weights* w, const float*
     if (!decode && start_pos + T > cache->t_max) return RDT_ERR_INVALID_ARG;
     max_keys = std::max(max_keys, cache->t_max);
   }
-  if (decode && (!cache || !cache_len)) return RDT_ERR_INVALID_ARG;
+  if (paged) {
+    if ((st = check_paged(c, paged, B, T, start_pos, n_loops)) != RDT_OK) return st;
+    max_keys = std::max(max_keys, paged->max_pages * paged->page_size);
+  }
+  if (decode && ((!cache && !paged) || !cache_len)) return RDT_ERR_INVALID_ARG;
   if (trace && (trace->row0 < 0 || trace->n_rows < 0 || trace->row0 + trace->n_rows > B * T)) return RDT_ERR_INVALID_ARG;
   Ctx x;
   x.c = c; x.w = w; x.ws = ws; x.s = s; x.dtype = c->dtype;
   make_layout(c, B, T, max_keys, &x.L);
+  x.paged = paged;
+  x.paged_off = x.L.total;
   if ((st = check_ws(ws, ws_bytes, x.L)) != RDT_OK) return st;
+  if (paged && ws_bytes < x.L.total + paged_ws_bytes(c, paged, B, T, start_pos, decode)) return RDT_ERR_WORKSPACE;
   // halted rows drop out of the attention queries and the O projection (prefill with ACT,
   // keys from this call's rows)
-  x.compact_q = act_on && !decode && !(cache && cache->k && start_pos > 0);
+  x.compact_q = act_on && !decode && !((paged || (cache && cache->k)) && start_pos > 0);
   x.st = at<DevStatus*>(ws, x.L.status);
   const int N = B * T, D = c->dim, E = c->n_experts;
   const bool transformer_off = (flags & RDT_FLAG_TRANSFORMER_OFF) != 0;
@@ -541,7 +609,7 @@ rdt_status run_recurrent(const rdt_config* c, const rdt_weights* w, const float*
   if (cudaMemsetAsync(at<void*>(ws, x.L.halted), 0, (size_t)N * 4, s) != cudaSuccess) return RDT_ERR_CUDA;
   launch_lti_A(w->log_A, w->log_dt, at<float*>(ws, x.L.Avec), D, s);
   launch_rope_table(at<float2*>(ws, x.L.rope), x.L.rope_pos, x.L.rope_dim, c->rope_theta, s);
-  if (decode) launch_positions_decode(pos, cache_len, B, cache->t_max, x.st, s);
+  if (decode) launch_positions_decode(pos, cache_len, B, paged ? paged->max_pages * paged->page_size : cache->t_max, x.st, s);
   else launch_positions(pos, N, T, start_pos, s);
   launch_iota(at<int*>(ws, x.L.run_list), at<int*>(ws, x.L.run_idx), at<int*>(ws, x.L.nrun), N, s);
   CombineParams cp = combine_base(x, N);
@@ -839,9 +907,9 @@ rdt_status rdt_recurrent_decode_step_ex(const rdt_config* cfg, const rdt_weights
                        halt_weights, expert_ids, cache, trace, 0, ws, ws_bytes, (cudaStream_t)stream, true);
 }
 
-rdt_status rdt_block_forward_cached(const rdt_config* cfg, const rdt_weights* w, const float* x_in, float* x_out,
-                                    int batch, int seq, int start_pos, const int32_t* cache_len,
-                                    const rdt_kv_cache* cache, void* ws, size_t ws_bytes, void* stream) {
+static rdt_status block_forward(const rdt_config* cfg, const rdt_weights* w, const float* x_in, float* x_out, int batch,
+                                int seq, int start_pos, const int32_t* cache_len, const rdt_kv_cache* cache,
+                                const rdt_paged_cache* paged, void* ws, size_t ws_bytes, void* stream) {
   rdt_status st = check_config(cfg);
   if (st != RDT_OK) return st;
   const bool moe = cfg->n_experts > 0;
@@ -856,18 +924,26 @@ rdt_status rdt_block_forward_cached(const rdt_config* cfg, const rdt_weights* w,
     if (!decode && start_pos + seq > cache->t_max) return RDT_ERR_INVALID_ARG;
     max_keys = std::max(max_keys, cache->t_max);
   }
-  if (decode && (!cache || seq != 1)) return RDT_ERR_INVALID_ARG;
+  if (paged) {
+    if ((st = check_paged(cfg, paged, batch, seq, start_pos, 1)) != RDT_OK) return st;
+    max_keys = std::max(max_keys, paged->max_pages * paged->page_size);
+  }
+  if (decode && ((!cache && !paged) || seq != 1)) return RDT_ERR_INVALID_ARG;
   cudaStream_t s = (cudaStream_t)stream;
   ProfScope ps_block(PC_BLOCK, s);
   Ctx x;
   x.c = cfg; x.w = w; x.ws = ws; x.s = s; x.dtype = cfg->dtype;
   make_layout(cfg, batch, seq, max_keys, &x.L);
+  x.paged = paged;
+  x.paged_off = x.L.total;
   if ((st = check_ws(ws, ws_bytes, x.L)) != RDT_OK) return st;
+  if (paged && ws_bytes < x.L.total + paged_ws_bytes(cfg, paged, batch, seq, start_pos, decode)) return RDT_ERR_WORKSPACE;
   x.st = at<DevStatus*>(ws, x.L.status);
   const int N = batch * seq, D = cfg->dim, F = cfg->expert_dim;
   if (cudaMemsetAsync(x.st, 0, sizeof(DevStatus), s) != cudaSuccess) return RDT_ERR_CUDA;
   launch_rope_table(at<float2*>(ws, x.L.rope), x.L.rope_pos, x.L.rope_dim, cfg->rope_theta, s);
-  if (decode) launch_positions_decode(at<int*>(ws, x.L.pos), cache_len, batch, cache->t_max, x.st, s);
+  if (decode) launch_positions_decode(at<int*>(ws, x.L.pos), cache_len, batch,
+                                      paged ? paged->max_pages * paged->page_size : cache->t_max, x.st, s);
   else launch_positions(at<int*>(ws, x.L.pos), N, seq, start_pos, s);
   void* a = at<void*>(ws, x.L.a);
   float* x1 = at<float*>(ws, x.L.x1);
@@ -893,6 +969,51 @@ rdt_status rdt_block_forward_cached(const rdt_config* cfg, const rdt_weights* w,
   }
   if (cudaGetLastError() != cudaSuccess) return RDT_ERR_CUDA;
   return RDT_OK;
+}
+
+rdt_status rdt_block_forward_cached(const rdt_config* cfg, const rdt_weights* w, const float* x_in, float* x_out,
+                                    int batch, int seq, int start_pos, const int32_t* cache_len,
+                                    const rdt_kv_cache* cache, void* ws, size_t ws_bytes, void* stream) {
+  return block_forward(cfg, w, x_in, x_out, batch, seq, start_pos, cache_len, cache, nullptr, ws, ws_bytes, stream);
+}
+
+rdt_status rdt_block_forward_paged(const rdt_config* cfg, const rdt_weights* w, const float* x_in, float* x_out, int batch,
+                                   int seq, int start_pos, const int32_t* cache_len, const rdt_paged_cache* cache, void* ws,
+                                   size_t ws_bytes, void* stream) {
+  if (!cache) return RDT_ERR_INVALID_ARG;
+  return block_forward(cfg, w, x_in, x_out, batch, seq, start_pos, cache_len, nullptr, cache, ws, ws_bytes, stream);
+}
+
+size_t rdt_paged_workspace_size(const rdt_config* cfg, int batch, int seq, int start_pos, const rdt_paged_cache* cache) {
+  if (check_config(cfg) != RDT_OK || batch <= 0 || seq <= 0 || start_pos < 0 ||
+      check_paged(cfg, cache, batch, seq, start_pos, 1) != RDT_OK)
+    return 0;
+  Layout L;
+  make_layout(cfg, batch, seq, cache->max_pages * cache->page_size, &L);
+  // one token may be a decode step or a prefill of one
+  size_t more = paged_ws_bytes(cfg, cache, batch, seq, start_pos, false);
+  if (seq == 1) more = std::max(more, paged_ws_bytes(cfg, cache, batch, 1, 0, true));
+  return L.total + more;
+}
+
+rdt_status rdt_recurrent_forward_paged(const rdt_config* cfg, const rdt_weights* w, const float* h0, const void* e,
+                                       int batch, int seq, int start_pos, int n_loops, float act_threshold,
+                                       const float* halt_logit_offset, float* h_out, float* halt_weights,
+                                       int32_t* expert_ids, const rdt_paged_cache* cache, const rdt_trace* trace,
+                                       void* ws, size_t ws_bytes, void* stream) {
+  if (!cache) return RDT_ERR_INVALID_ARG;
+  return run_recurrent(cfg, w, h0, e, batch, seq, start_pos, nullptr, n_loops, act_threshold, halt_logit_offset, h_out,
+                       halt_weights, expert_ids, nullptr, trace, 0, ws, ws_bytes, (cudaStream_t)stream, false, cache);
+}
+
+rdt_status rdt_recurrent_decode_step_paged(const rdt_config* cfg, const rdt_weights* w, const float* h0, const void* e,
+                                           int batch, const int32_t* cache_len, int n_loops, float act_threshold,
+                                           const float* halt_logit_offset, float* h_out, float* halt_weights,
+                                           int32_t* expert_ids, const rdt_paged_cache* cache, const rdt_trace* trace,
+                                           void* ws, size_t ws_bytes, void* stream) {
+  if (!cache) return RDT_ERR_INVALID_ARG;
+  return run_recurrent(cfg, w, h0, e, batch, 1, 0, cache_len, n_loops, act_threshold, halt_logit_offset, h_out,
+                       halt_weights, expert_ids, nullptr, trace, 0, ws, ws_bytes, (cudaStream_t)stream, true, cache);
 }
 
 rdt_status rdt_block_forward(const rdt_config* cfg, const rdt_weights* w, const float* x_in, float* x_out, int batch,

@@ -104,3 +104,26 @@ def test_python_checks():
         R.sample_tokens(z(2, 5, dt=torch.float32), z(2, dt=torch.float32))
     with pytest.raises(ValueError):
         R.PagedKVCache.alloc(RI.get_workload("tiny_mla_fp32").cfg, 1, 2, 32)
+
+
+def test_paged_model_calls_refuse(nat):
+    """The model's paged entry points: host checks (no launch is reached)."""
+    from recurrent_depth_moe_b200 import api
+    lib = nat.load()
+    gqa = api.config_struct(RI.get_workload("tiny_gqa_fp32").cfg)
+    mla = api.config_struct(RI.get_workload("tiny_mla_fp32").cfg)
+    fits = dict(dtype=0, n_kv_heads=2, head_dim=32)
+    size = lambda cs, b=2, s=1, start=0, **kw: lib.rdt_paged_workspace_size(ctypes.byref(cs), b, s, start,
+                                                                            ctypes.byref(_cache(nat, **{**fits, **kw})))
+    assert size(gqa) > 0 and size(gqa) % 256 == 0
+    assert size(gqa, s=16, start=16) > size(gqa, s=16)               # the positions read back
+    for kw in (dict(dtype=1), dict(n_kv_heads=4), dict(head_dim=64), dict(batch=1), dict(kv_type=1), dict(max_pages=0)):
+        assert size(gqa, **kw) == 0, kw
+    assert size(mla) == 0 and size(gqa, b=0) == 0 and size(gqa, s=0) == 0 and size(gqa, start=-1) == 0
+    assert size(gqa, s=16, start=17) == 0                            # past the table
+    w = nat.rdt_weights()
+    r, wr = ctypes.byref(gqa), ctypes.byref(w)
+    none = [None, None, P, 1 << 30, None]
+    assert lib.rdt_recurrent_decode_step_paged(r, wr, P, P, 2, P, 1, 0.0, None, P, P, P, None, None, P, 1 << 30, None) == 1
+    assert lib.rdt_recurrent_forward_paged(r, wr, P, P, 2, 4, 0, 1, 0.0, None, P, P, P, *none) == 1
+    assert lib.rdt_block_forward_paged(r, wr, P, P + 256, 2, 4, 0, None, None, P, 1 << 30, None) == 1
