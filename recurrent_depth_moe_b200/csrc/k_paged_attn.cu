@@ -576,6 +576,8 @@ __global__ void __launch_bounds__(32 * WARPS, HD <= 128 ? Tile<Q>::CTAS : 1) k_p
   // become the output if the group lies within the CTA, else the CTA's part
   __syncthreads();
   Desc joins{-1, 0, 0, 0};
+  const int first = gridDim.x + blockIdx.x * WARPS;   // of the warps' parts
+  int item = 0;
   for (int i = 0; i < 2 * WARPS;) {
     const long long id = run_id[i];
     if (id < 0) {
@@ -589,35 +591,33 @@ __global__ void __launch_bounds__(32 * WARPS, HD <= 128 ? Tile<Q>::CTAS : 1) k_p
     const int b = (int)(id / segs), seg = (int)(id % segs), g = seg / n_ht, h0 = seg % n_ht * GT, nh = min(GT, G - h0);
     if (!begun && ended) joins = Desc{b, seg, run_first[last >> 1], 0};
     for (int h = 0; h < nh; ++h) {
-      float M = -INFINITY, L = 0.f, w[2 * WARPS];
-#pragma unroll
-      for (int k = 0; k < 2 * WARPS; ++k) {
-        const bool in = k >= i && k <= last && run_id[k] == id;
-        w[k] = in ? part_ml(p, gridDim.x + blockIdx.x * WARPS + (k >> 1), k & 1)[h * 2] : -INFINITY;
-        M = fmaxf(M, w[k]);
-      }
-      const float base = M == -INFINITY ? 0.f : M;
-#pragma unroll
-      for (int k = 0; k < 2 * WARPS; ++k) {
-        const bool in = k >= i && k <= last && run_id[k] == id;
-        w[k] = in ? ex2(w[k] - base) : 0.f;
-        if (in) L += w[k] * part_ml(p, gridDim.x + blockIdx.x * WARPS + (k >> 1), k & 1)[h * 2 + 1];
-      }
-      for (int ch = threadIdx.x; ch < hd; ch += 32 * WARPS) {
-        float o = 0.f;
+      if ((item++ & (WARPS - 1)) != warp) continue;   // a warp per (group, head)
+      const int part = lane < 2 * WARPS && lane >= i && lane <= last && run_id[lane] == id ? lane : -1;
+      const float2 ml = part >= 0 ? *reinterpret_cast<const float2*>(part_ml(p, first + (part >> 1), part & 1) + h * 2)
+                                  : make_float2(-INFINITY, 0.f);
+      const float M = warp_max(ml.x), base = M == -INFINITY ? 0.f : M;
+      const float w = ex2(ml.x - base), L = warp_sum(w * ml.y), inv = begun && ended ? (L != 0.f ? 1.f / L : 0.f) : 1.f;
+      const unsigned parts = __ballot_sync(0xffffffffu, part >= 0);
+      for (int ch = 4 * lane; ch < (hd + 127) / 128 * 128; ch += 128) {
+        float4 v[2 * WARPS], o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int k = 0; k < 2 * WARPS; ++k)
-          if (k >= i && k <= last && run_id[k] == id)
-            o = fmaf(w[k], part_o(p, gridDim.x + blockIdx.x * WARPS + (k >> 1), k & 1)[h * hd + ch], o);
-        if (begun && ended)
-          ((bf16*)p.o)[(long long)b * p.o_row + (long long)(g * G + h0 + h) * hd + ch] = from_f<bf16>(L != 0.f ? o / L : 0.f);
-        else
-          part_o(p, blockIdx.x, begun)[h * hd + ch] = o;
+          if ((parts >> k & 1) && ch < hd)
+            v[k] = *reinterpret_cast<const float4*>(part_o(p, first + (k >> 1), k & 1) + h * hd + ch);
+#pragma unroll
+        for (int k = 0; k < 2 * WARPS; ++k) {
+          const float wk = __shfl_sync(0xffffffffu, w, k);
+          if (parts >> k & 1) o.x = fmaf(wk, v[k].x, o.x), o.y = fmaf(wk, v[k].y, o.y), o.z = fmaf(wk, v[k].z, o.z), o.w = fmaf(wk, v[k].w, o.w);
+        }
+        if (ch >= hd) continue;
+        if (begun && ended) {
+          bf16* y = (bf16*)p.o + (long long)b * p.o_row + (long long)(g * G + h0 + h) * hd + ch;
+          y[0] = from_f<bf16>(o.x * inv), y[1] = from_f<bf16>(o.y * inv), y[2] = from_f<bf16>(o.z * inv), y[3] = from_f<bf16>(o.w * inv);
+        } else {
+          *reinterpret_cast<float4*>(part_o(p, blockIdx.x, begun) + h * hd + ch) = o;
+        }
       }
-      if (threadIdx.x == 0 && !(begun && ended)) {
-        part_ml(p, blockIdx.x, begun)[h * 2] = M;
-        part_ml(p, blockIdx.x, begun)[h * 2 + 1] = L;
-      }
+      if (lane == 0 && !(begun && ended)) *reinterpret_cast<float2*>(part_ml(p, blockIdx.x, begun) + h * 2) = make_float2(M, L);
     }
     i = j;
   }
@@ -628,51 +628,62 @@ __global__ void __launch_bounds__(32 * WARPS, HD <= 128 ? Tile<Q>::CTAS : 1) k_p
 // ------------------------------------------------------------------------------------------
 // plain kernel: any width and page size, fp32 or bf16, both storage forms; a worker is a CTA
 // ------------------------------------------------------------------------------------------
-// 32-key tiles of K and V widened to fp32 in shared memory.  Scores: a lane per key, each warp
-// a quarter of the channels for all heads, so a K element serves 8 products; values: a thread
-// per channel, so a V element serves 8.  Bound by shared-memory loads (3 per 8 products).
+// 32-key tiles of K and V in fp32 in shared memory, NH (1, 2, 4 or 8) query heads at a time.
+// Scores: a lane per key, each warp a quarter of the channels for all heads, so a K element
+// serves NH products; values: a thread per channel, so a V element serves NH.  An fp32 cache is
+// copied by cp.async one tile ahead; the other forms are widened on the way.
 namespace {
 constexpr int TK = 32;
 struct PlainSm {
-  long long* slot;   // [TK] slot of each key, -1: takes no part
-  float* q;          // [hd][GT]
-  float* k;          // [TK][ld]
-  float* v;          // [TK][ld]
-  float* part;       // [WARPS][GT][TK]
-  float* w;          // [TK][GT]
-  float* corr;       // [GT]
-  int ld;
   __host__ __device__ static int stride(int hd) { return (hd + 3) / 4 * 4 + 4; }   // 4 mod 32 words: no conflicts
-  __host__ __device__ static size_t bytes(int hd) {
-    return TK * 8 + sizeof(float) * ((size_t)GT * ((hd + 3) / 4 * 4) + 2 * (size_t)TK * stride(hd) + WARPS * GT * TK + TK * GT + GT);
+  __host__ __device__ static size_t tile(int hd) { return 2 * (size_t)TK * stride(hd); }   // floats: K then V
+  __host__ __device__ static size_t bytes(int hd, int nh, int buffers) {
+    return buffers * TK * 8 + sizeof(float) * ((size_t)nh * ((hd + 3) / 4 * 4) + buffers * tile(hd) + WARPS * nh * TK + TK * nh + GT);
   }
 };
+template <int NH> struct Heads { float x[NH]; };
+template <int NH> __device__ __forceinline__ Heads<NH> heads_at(const float* p) {   // aligned to NH floats
+  Heads<NH> r;
+  if (NH == 8) {
+    const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+    r.x[0] = a.x; r.x[1 % NH] = a.y; r.x[2 % NH] = a.z; r.x[3 % NH] = a.w;
+    r.x[4 % NH] = b.x; r.x[5 % NH] = b.y; r.x[6 % NH] = b.z; r.x[7 % NH] = b.w;
+  } else if (NH == 4) {
+    const float4 a = *reinterpret_cast<const float4*>(p);
+    r.x[0] = a.x; r.x[1 % NH] = a.y; r.x[2 % NH] = a.z; r.x[3 % NH] = a.w;
+  } else if (NH == 2) {
+    const float2 a = *reinterpret_cast<const float2*>(p);
+    r.x[0] = a.x; r.x[1 % NH] = a.y;
+  } else {
+    r.x[0] = *p;
+  }
+  return r;
+}
 }  // namespace
 
-template <typename T, bool Q>
-__global__ void __launch_bounds__(128) k_paged_attn_simt(PagedAttnParams p, int least, int vec) {
+template <typename T, bool Q, int NH, bool VEC>
+__global__ void __launch_bounds__(128) k_paged_attn_simt(PagedAttnParams p, int least) {
+  constexpr bool AHEAD = VEC && !Q && sizeof(T) == 4;   // copied as it is, a tile ahead
+  constexpr int BUF = AHEAD ? 2 : 1, HW = (NH + WARPS - 1) / WARPS;   // heads of a warp
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ long long red[WARPS];
   __shared__ int kept[LENS];
   const int hd = p.c.hd, hd4 = (hd + 3) / 4 * 4, Hkv = p.c.Hkv, G = p.H / Hkv, n_ht = (G + GT - 1) / GT, segs = Hkv * n_ht;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  PlainSm sm;
-  sm.ld = PlainSm::stride(hd);
-  sm.slot = reinterpret_cast<long long*>(smem);
-  sm.q = reinterpret_cast<float*>(sm.slot + TK);
-  sm.k = sm.q + GT * hd4;
-  sm.v = sm.k + TK * sm.ld;
-  sm.part = sm.v + TK * sm.ld;
-  sm.w = sm.part + WARPS * GT * TK;
-  sm.corr = sm.w + TK * GT;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, ld = PlainSm::stride(hd);
+  long long* slot_s = reinterpret_cast<long long*>(smem);       // [BUF][TK] slot of each key, -1: takes no part
+  float* qs = reinterpret_cast<float*>(slot_s + BUF * TK);      // [hd4][NH]
+  float* kv = qs + NH * hd4;                                    // [BUF][2][TK][ld]
+  float* part = kv + BUF * 2 * TK * ld;                         // [WARPS][NH][TK]
+  float* ws = part + WARPS * NH * TK;                           // [TK][NH]
+  float* corr_s = ws + TK * NH;                                 // [GT]
   const long long length = line_length(p, segs, TK, kept, red);
   const Lens lens{p, p.B <= LENS ? kept : nullptr};
   zero_rows(p, lens, (int)sizeof(T));
   const long long piece = piece_of(length, gridDim.x, least);
   const long long w0 = blockIdx.x * piece, w1 = w0 + piece < length ? w0 + piece : length;
   // channels past the width (up to a multiple of 4) are zeros in q and K
-  for (int i = tid; i < GT * hd4; i += 128) sm.q[i] = 0.f;
-  for (int i = tid; i < TK * sm.ld; i += 128) sm.k[i] = sm.v[i] = 0.f;
+  for (int i = tid; i < NH * hd4; i += 128) qs[i] = 0.f;
+  for (int i = tid; i < BUF * 2 * TK * ld; i += 128) kv[i] = 0.f;
   Desc joins{-1, 0, 0, 0};
   Place at = w0 < w1 ? line_find(lens, segs, TK, w0) : Place{0, 0};
   for (long long x = w0; x < w1;) {
@@ -687,21 +698,24 @@ __global__ void __launch_bounds__(128) k_paged_attn_simt(PagedAttnParams p, int 
     x += u1 - u0;
     at.at += u1 - u0;
     if (t0 == t1) continue;
-    const int g = seg / n_ht, h0 = seg % n_ht * GT, nh = min(GT, G - h0);
+    const int g = seg / n_ht, h0 = seg % n_ht * GT, nh = min(GT, G - h0);   // nh <= NH
+    const bool whole = t0 == 0 && t1 == nt;
+    const int which = t0 == 0;
+    if (t0 > 0 && t1 == nt) joins = Desc{b, seg, (int)((begin + START) / piece), 0};
     const float sl2 = p.scale * LOG2E;
     __syncthreads();
     for (int i = tid; i < nh * hd; i += 128) {
       const int h = i / hd, d = i - h * hd;
-      sm.q[d * GT + h] = to_f(((const T*)p.q)[(long long)b * p.q_row + (long long)(g * G + h0) * hd + i]) * sl2;
+      qs[d * NH + h] = to_f(((const T*)p.q)[(long long)b * p.q_row + (long long)(g * G + h0) * hd + i]) * sl2;
     }
-    if (nh < GT)
-      for (int i = tid; i < (GT - nh) * hd; i += 128) sm.q[i / (GT - nh) * GT + nh + i % (GT - nh)] = 0.f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};       // heads warp and warp + 4
-    float acc[GT][2];                                             // channels tid and tid + 128
+    if (nh < NH)
+      for (int i = tid; i < (NH - nh) * hd; i += 128) qs[i / (NH - nh) * NH + nh + i % (NH - nh)] = 0.f;
+    float m[HW], l[HW], acc[NH][2];                           // heads warp + 4 u; channels tid and tid + 128
 #pragma unroll
-    for (int h = 0; h < GT; ++h) acc[h][0] = acc[h][1] = 0.f;
-    for (int t = t0; t < t1; ++t) {
-      __syncthreads();
+    for (int u = 0; u < HW; ++u) m[u] = -INFINITY, l[u] = 0.f;
+#pragma unroll
+    for (int h = 0; h < NH; ++h) acc[h][0] = acc[h][1] = 0.f;
+    auto find_slots = [&](int t) {
       if (tid < TK) {
         const int key = t * TK + tid;
         long long s = -1;
@@ -709,15 +723,24 @@ __global__ void __launch_bounds__(128) k_paged_attn_simt(PagedAttnParams p, int 
           const int page = page_of(p.c, b, key, p.st, 222);
           if (page >= 0) s = ((long long)page * Hkv + g) * p.c.page_size + key % p.c.page_size;
         }
-        sm.slot[tid] = s;
+        slot_s[(t & (BUF - 1)) * TK + tid] = s;
       }
-      __syncthreads();
-      // masked rows hold zeros: 0 * v is 0 whatever the slot holds
-      if (vec) {
+    };
+    // masked rows hold zeros: 0 * v is 0 whatever the slot holds
+    auto copy = [&](int t) {
+      const long long* slots = slot_s + (t & (BUF - 1)) * TK;
+      float *k = kv + (t & (BUF - 1)) * 2 * TK * ld, *v = k + TK * ld;
+      if (VEC) {
         const int q4 = hd / 4;
         for (int i = tid; i < TK * q4; i += 128) {
           const int r = i / q4, c = i - r * q4;
-          const long long s = sm.slot[r];
+          const long long s = slots[r];
+          if (AHEAD) {
+            const long long off = s >= 0 ? s * q4 + c : 0;
+            cp16_or_zero(smem_addr(k + r * ld + 4 * c), (const float4*)p.c.k + off, s >= 0);
+            cp16_or_zero(smem_addr(v + r * ld + 4 * c), (const float4*)p.c.v + off, s >= 0);
+            continue;
+          }
           float4 kx = make_float4(0.f, 0.f, 0.f, 0.f), vx = kx;
           if (s >= 0) {
             if (Q) {
@@ -725,9 +748,6 @@ __global__ void __launch_bounds__(128) k_paged_attn_simt(PagedAttnParams p, int 
               const float ks = exp_byte_scale(p.c.ke[s]), vs = exp_byte_scale(p.c.ve[s]);
               kx = make_float4(e4m3_f(kw & 255) * ks, e4m3_f(kw >> 8 & 255) * ks, e4m3_f(kw >> 16 & 255) * ks, e4m3_f(kw >> 24) * ks);
               vx = make_float4(e4m3_f(vw & 255) * vs, e4m3_f(vw >> 8 & 255) * vs, e4m3_f(vw >> 16 & 255) * vs, e4m3_f(vw >> 24) * vs);
-            } else if (sizeof(T) == 4) {
-              kx = __ldg((const float4*)p.c.k + s * q4 + c);
-              vx = __ldg((const float4*)p.c.v + s * q4 + c);
             } else {
               const uint2 kw = __ldg((const uint2*)p.c.k + s * q4 + c), vw = __ldg((const uint2*)p.c.v + s * q4 + c);
               kx = make_float4(__uint_as_float(kw.x << 16), __uint_as_float(kw.x & 0xffff0000u), __uint_as_float(kw.y << 16),
@@ -736,13 +756,13 @@ __global__ void __launch_bounds__(128) k_paged_attn_simt(PagedAttnParams p, int 
                                __uint_as_float(vw.y & 0xffff0000u));
             }
           }
-          *reinterpret_cast<float4*>(sm.k + r * sm.ld + 4 * c) = kx;
-          *reinterpret_cast<float4*>(sm.v + r * sm.ld + 4 * c) = vx;
+          *reinterpret_cast<float4*>(k + r * ld + 4 * c) = kx;
+          *reinterpret_cast<float4*>(v + r * ld + 4 * c) = vx;
         }
       } else {
         for (int i = tid; i < TK * hd; i += 128) {
           const int r = i / hd, d = i - r * hd;
-          const long long s = sm.slot[r];
+          const long long s = slots[r];
           float kx = 0.f, vx = 0.f;
           if (s >= 0) {
             if (Q) {
@@ -753,45 +773,61 @@ __global__ void __launch_bounds__(128) k_paged_attn_simt(PagedAttnParams p, int 
               vx = to_f(((const T*)p.c.v)[s * hd + d]);
             }
           }
-          sm.k[r * sm.ld + d] = kx;
-          sm.v[r * sm.ld + d] = vx;
+          k[r * ld + d] = kx;
+          v[r * ld + d] = vx;
         }
       }
+      if (AHEAD) cp_commit();
+    };
+    if (AHEAD) {
+      find_slots(t0);
       __syncthreads();
+      copy(t0);
+    }
+    for (int t = t0; t < t1; ++t) {
+      if (!AHEAD) __syncthreads();                            // the tile before is done with
+      const int tn = AHEAD ? t + 1 : t;
+      if (tn < t1) find_slots(tn);
+      __syncthreads();
+      if (tn < t1) copy(tn);
+      else if (AHEAD) cp_commit();
+      if (AHEAD) cp_wait<1>();
+      __syncthreads();
+      const float *k = kv + (t & (BUF - 1)) * 2 * TK * ld, *v = k + TK * ld;
       {
         const int n4 = hd4 / 4, c0 = n4 * warp / WARPS, c1 = n4 * (warp + 1) / WARPS;
-        float s[GT] = {};
+        float s[NH] = {};
+#pragma unroll 2
         for (int c = c0; c < c1; ++c) {
-          const float4 k4 = *reinterpret_cast<const float4*>(sm.k + lane * sm.ld + 4 * c);
+          const float4 k4 = *reinterpret_cast<const float4*>(k + lane * ld + 4 * c);
           const float kk[4] = {k4.x, k4.y, k4.z, k4.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float4 qa = *reinterpret_cast<const float4*>(sm.q + (4 * c + e) * GT);
-            const float4 qb = *reinterpret_cast<const float4*>(sm.q + (4 * c + e) * GT + 4);
-            s[0] = fmaf(qa.x, kk[e], s[0]); s[1] = fmaf(qa.y, kk[e], s[1]);
-            s[2] = fmaf(qa.z, kk[e], s[2]); s[3] = fmaf(qa.w, kk[e], s[3]);
-            s[4] = fmaf(qb.x, kk[e], s[4]); s[5] = fmaf(qb.y, kk[e], s[5]);
-            s[6] = fmaf(qb.z, kk[e], s[6]); s[7] = fmaf(qb.w, kk[e], s[7]);
+            const Heads<NH> q = heads_at<NH>(qs + (4 * c + e) * NH);
+#pragma unroll
+            for (int h = 0; h < NH; ++h) s[h] = fmaf(q.x[h], kk[e], s[h]);
           }
         }
 #pragma unroll
-        for (int h = 0; h < GT; ++h) sm.part[(warp * GT + h) * TK + lane] = s[h];
+        for (int h = 0; h < NH; ++h) part[(warp * NH + h) * TK + lane] = s[h];
       }
       __syncthreads();
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int h = warp + 4 * u;
-        float s = 0.f;
+      for (int u = 0; u < HW; ++u) {
+        const int h = warp + WARPS * u;
+        if (h < NH) {
+          float s = 0.f;
 #pragma unroll
-        for (int w = 0; w < WARPS; ++w) s += sm.part[(w * GT + h) * TK + lane];
-        if (sm.slot[lane] < 0) s = -INFINITY;
-        const float mx = fmaxf(m[u], warp_max(s));
-        const float base = mx == -INFINITY ? 0.f : mx;
-        const float e = exp2f(s - base), c = exp2f(m[u] - base);
-        m[u] = mx;
-        l[u] = l[u] * c + warp_sum(e);
-        sm.w[lane * GT + h] = e;
-        if (lane == 0) sm.corr[h] = c;
+          for (int w = 0; w < WARPS; ++w) s += part[(w * NH + h) * TK + lane];
+          if (slot_s[(t & (BUF - 1)) * TK + lane] < 0) s = -INFINITY;
+          const float mx = fmaxf(m[u], warp_max(s));
+          const float base = mx == -INFINITY ? 0.f : mx;
+          const float e = exp2f(s - base), c = exp2f(m[u] - base);
+          m[u] = mx;
+          l[u] = l[u] * c + warp_sum(e);
+          ws[lane * NH + h] = e;
+          if (lane == 0) corr_s[h] = c;
+        }
       }
       __syncthreads();
 #pragma unroll
@@ -799,32 +835,30 @@ __global__ void __launch_bounds__(128) k_paged_attn_simt(PagedAttnParams p, int 
         const int d = tid + 128 * u;
         if (d < hd) {
 #pragma unroll
-          for (int h = 0; h < GT; ++h) acc[h][u] *= sm.corr[h];
+          for (int h = 0; h < NH; ++h) acc[h][u] *= corr_s[h];
 #pragma unroll 8
           for (int r = 0; r < TK; ++r) {
-            const float v = sm.v[r * sm.ld + d];
-            const float4 wa = *reinterpret_cast<const float4*>(sm.w + r * GT), wb = *reinterpret_cast<const float4*>(sm.w + r * GT + 4);
-            acc[0][u] = fmaf(wa.x, v, acc[0][u]); acc[1][u] = fmaf(wa.y, v, acc[1][u]);
-            acc[2][u] = fmaf(wa.z, v, acc[2][u]); acc[3][u] = fmaf(wa.w, v, acc[3][u]);
-            acc[4][u] = fmaf(wb.x, v, acc[4][u]); acc[5][u] = fmaf(wb.y, v, acc[5][u]);
-            acc[6][u] = fmaf(wb.z, v, acc[6][u]); acc[7][u] = fmaf(wb.w, v, acc[7][u]);
+            const float vx = v[r * ld + d];
+            const Heads<NH> w = heads_at<NH>(ws + r * NH);
+#pragma unroll
+            for (int h = 0; h < NH; ++h) acc[h][u] = fmaf(w.x[h], vx, acc[h][u]);
           }
         }
       }
     }
-    const bool whole = t0 == 0 && t1 == nt;
-    const int which = t0 == 0;
-    if (t0 > 0 && t1 == nt) joins = Desc{b, seg, (int)((begin + START) / piece), 0};
+    if (AHEAD) cp_wait<0>();
     __syncthreads();
     if (lane == 0) {
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int h = warp + 4 * u;
-        sm.corr[h] = l[u];
-        if (!whole) {
-          float* ml = part_ml(p, blockIdx.x, which);
-          ml[h * 2] = m[u];
-          ml[h * 2 + 1] = l[u];
+      for (int u = 0; u < HW; ++u) {
+        const int h = warp + WARPS * u;
+        if (h < NH) {
+          corr_s[h] = l[u];
+          if (!whole && h < nh) {
+            float* ml = part_ml(p, blockIdx.x, which);
+            ml[h * 2] = m[u];
+            ml[h * 2 + 1] = l[u];
+          }
         }
       }
     }
@@ -834,11 +868,11 @@ __global__ void __launch_bounds__(128) k_paged_attn_simt(PagedAttnParams p, int 
       const int d = tid + 128 * u;
       if (d >= hd) continue;
 #pragma unroll
-      for (int h = 0; h < GT; ++h) {
+      for (int h = 0; h < NH; ++h) {
         if (h >= nh) continue;
         if (whole)
           ((T*)p.o)[(long long)b * p.o_row + (long long)(g * G + h0 + h) * hd + d] =
-              from_f<T>(sm.corr[h] != 0.f ? acc[h][u] / sm.corr[h] : 0.f);
+              from_f<T>(corr_s[h] != 0.f ? acc[h][u] / corr_s[h] : 0.f);
         else
           part_o(p, blockIdx.x, which)[h * hd + d] = acc[h][u];
       }
@@ -921,7 +955,7 @@ bool mma_takes(int dtype, const PagedView& c) {
   return dtype == 1 && c.hd % 8 == 0 && rb % 16 == 0 && !(((uintptr_t)c.k | (uintptr_t)c.v) & 15);
 }
 int ctas_mma(bool e4m3) { return device_sm_count() * (e4m3 ? Tile<true>::CTAS : Tile<false>::CTAS); }
-int ctas_simt() { return device_sm_count() * 4; }
+int ctas_simt() { return device_sm_count() * 3; }   // (an fp32 tile of 128 channels, twice, is 68 KB)
 // descriptors, then the parts of `ctas` CTAs and, on tensor cores, of their warps
 size_t scratch_bytes(int ctas, int parts, int hd) {
   return (size_t)ctas * sizeof(Desc) + (size_t)parts * 2 * GT * (hd + 2) * sizeof(float);
@@ -980,18 +1014,30 @@ int launch_paged_attn(int dtype, const PagedAttnParams& p0, cudaStream_t s) {
     note_launch();
     return launch_join<bf16>(p, ctas, s);
   }
-  const int smem = (int)PlainSm::bytes(p.c.hd), most = (int)PlainSm::bytes(256);
-  const int eb = p.c.e4m3 ? 1 : dtype == 0 ? 4 : 2;
-  const int vec = p.c.hd % 4 == 0 && !(((uintptr_t)p.c.k | (uintptr_t)p.c.v) & (4 * eb - 1));
-#define RDT_SIMT(TT, QQ)                                                                      do {                                                                                          if (!ensure_smem_limit((const void*)k_paged_attn_simt<TT, QQ>, most)) return -1;            k_paged_attn_simt<TT, QQ><<<ctas, 128, smem, s>>>(p, 3, vec);                          } while (0)
+  const int eb = p.c.e4m3 ? 1 : dtype == 0 ? 4 : 2, G = p.H / p.c.Hkv;
+  const bool vec = p.c.hd % 4 == 0 && !(((uintptr_t)p.c.k | (uintptr_t)p.c.v) & (4 * eb - 1));
+  const int nh = G >= 5 ? 8 : G >= 3 ? 4 : G, buffers = vec && dtype == 0 && !p.c.e4m3 ? 2 : 1;
+  const int smem = (int)PlainSm::bytes(p.c.hd, nh, buffers), most = (int)PlainSm::bytes(256, 8, 2);
+  void (*kernel)(PagedAttnParams, int) = nullptr;
+#define RDT_SIMT(TT, QQ, NN) kernel = vec ? k_paged_attn_simt<TT, QQ, NN, true> : k_paged_attn_simt<TT, QQ, NN, false>
+#define RDT_SIMT_H(TT, QQ)              \
+  do {                                  \
+    if (nh == 1) RDT_SIMT(TT, QQ, 1);   \
+    else if (nh == 2) RDT_SIMT(TT, QQ, 2); \
+    else if (nh == 4) RDT_SIMT(TT, QQ, 4); \
+    else RDT_SIMT(TT, QQ, 8);           \
+  } while (0)
   if (dtype == 0) {
-    if (p.c.e4m3) RDT_SIMT(float, true);
-    else RDT_SIMT(float, false);
+    if (p.c.e4m3) RDT_SIMT_H(float, true);
+    else RDT_SIMT_H(float, false);
   } else {
-    if (p.c.e4m3) RDT_SIMT(bf16, true);
-    else RDT_SIMT(bf16, false);
+    if (p.c.e4m3) RDT_SIMT_H(bf16, true);
+    else RDT_SIMT_H(bf16, false);
   }
+#undef RDT_SIMT_H
 #undef RDT_SIMT
+  if (!ensure_smem_limit((const void*)kernel, most)) return -1;
+  kernel<<<ctas, 128, smem, s>>>(p, 3);
   note_launch();
   return dtype == 0 ? launch_join<float>(p, ctas, s) : launch_join<bf16>(p, ctas, s);
 }
