@@ -38,6 +38,7 @@ namespace {
 constexpr int NWMAX = 16;        // warps of a CTA
 constexpr int BINS = 46 * 16;    // of the exponent: below 2^-46 a weight rounds to nothing
 constexpr int RB = 256;          // bins of one refinement
+constexpr int HB = BINS / 4;     // threads that sum the cluster's histograms, four bins each
 constexpr int LCAP = 1024;       // candidates one CTA lists; more are found by passes over the row
 constexpr int IDX_BITS = 20;
 constexpr int CMAX = 8;          // CTAs of a cluster
@@ -164,16 +165,16 @@ struct Sum {
   }
 };
 
-struct Shared {
-  u64 mass[2][RB];
+struct __align__(16) Shared {
+  u64 mass[2][RB];       // refinements: weight, and number, of the candidates by bin
   u64 wsum[NWMAX];       // kept weight of each warp's piece of the row
   u64 glist[2][32];      // [top-k, top-p] the last candidates
   u64 ranked[32];
   u64 red[NWMAX];
   u64 bc[3];
   u64 total, above;
-  uint32_t hist[BINS];
-  uint32_t cnt[2][RB];
+  __align__(16) uint32_t hist[BINS];
+  __align__(16) uint32_t cnt[2][RB];
   uint32_t list[LCAP];
   uint32_t fcnt[2], gcnt[2], kmin[2], kmax[2];
   uint32_t add[NWMAX][2], nranked;
@@ -271,7 +272,7 @@ struct Cut {
 __device__ __forceinline__ int bin_index(float b) { return __float_as_int(b) - __float_as_int(Weigh::MAGIC); }
 
 template <bool RES, int NT> struct Sampler {
-  static constexpr int NW = NT / 32, BPT = (BINS + NT - 1) / NT;   // bins of a thread
+  static constexpr int NW = NT / 32;
   cg::cluster_group cl;
   Shared& sh;
   const Row<RES>& row;
@@ -280,27 +281,36 @@ template <bool RES, int NT> struct Sampler {
   __device__ __forceinline__ Sampler(Shared& s, const Row<RES>& r, const Weigh& w)
       : cl(cg::this_cluster()), sh(s), row(r), wt(w), C((int)cl.num_blocks()), level(0) {}
 
-  // Sum of the cluster's histograms: bins BPT * thread + i.
-  __device__ __forceinline__ void counts(uint32_t (&c)[BPT]) {
-    uint32_t h[CMAX][BPT];                                       // remote reads, all in flight
+  // Sum of the cluster's histograms: bins 4 * thread + i (remote reads, all in flight; few and
+  // wide, since they cost by the request).
+  __device__ __forceinline__ void counts(uint32_t (&c)[4]) {
+    uint4 h[CMAX];
 #pragma unroll
     for (int r = 0; r < CMAX; ++r)
+      h[r] = r < C && threadIdx.x < HB ? reinterpret_cast<const uint4*>(cl.map_shared_rank(sh.hist, r))[threadIdx.x]
+                                       : make_uint4(0, 0, 0, 0);
+    c[0] = c[1] = c[2] = c[3] = 0;
 #pragma unroll
-      for (int i = 0; i < BPT; ++i) {
-        const int b = BPT * threadIdx.x + i;
-        h[r][i] = r < C && b < BINS ? cl.map_shared_rank(sh.hist, r)[b] : 0;
-      }
-#pragma unroll
-    for (int i = 0; i < BPT; ++i) {
-      c[i] = 0;
-#pragma unroll
-      for (int r = 0; r < CMAX; ++r) c[i] += h[r][i];
+    for (int r = 0; r < CMAX; ++r) c[0] += h[r].x, c[1] += h[r].y, c[2] += h[r].z, c[3] += h[r].w;
+  }
+  // Candidates' bins of a refinement: RB equal steps of the exponent over bins blo .. bhi.
+  struct Steps {
+    float lo, per;
+    __device__ __forceinline__ Steps(float blo, float bhi)
+        : lo(blo - Weigh::MAGIC - 0.5f), per((float)RB / (bhi - blo + 1.f)) {}
+    __device__ __forceinline__ int operator()(const Weigh& wt, float x) const {
+      return min(RB - 1, max(0, __float2int_rd(((wt.m - x) * wt.c16 - lo) * per)));
     }
+  };
+  __device__ __forceinline__ void clear_level(int par) {
+    for (int i = threadIdx.x; i < RB; i += NT) sh.mass[par][i] = 0, sh.cnt[par][i] = 0;
   }
   // One pass over the warp's piece: f(four elements, local index of the first) returns a bit
   // for each that is a candidate of phase ph.  A lane's bits of eight quads are kept in a
-  // register and listed together.
-  template <typename F> __device__ __forceinline__ void list_each4(int ph, F f) {
+  // register and listed together; each candidate also counts (with MASS its weight too) in the
+  // refinement `par`.
+  template <bool MASS, typename F>
+  __device__ __forceinline__ void list_each4(int ph, int par, const Steps& steps, F f) {
     const int lane = threadIdx.x & 31;
     uint32_t klo = ~0u, khi = 0;
     for (int j0 = row.jb; j0 < row.je; j0 += 256) {
@@ -321,10 +331,14 @@ template <bool RES, int NT> struct Sampler {
       at = __shfl_sync(0xffffffffu, at, 31) + incl - c;
       for (; bits; bits &= bits - 1, ++at) {
         const int e = __ffs(bits) - 1, l = 4 * (j0 + 32 * (e >> 2) + lane) + (e & 3);
-        const uint32_t k = key_of(row.at(l));
+        const float x = row.at(l);
+        const uint32_t k = key_of(x);
+        const int b = steps(wt, x);
         klo = min(klo, k);
         khi = max(khi, k);
         if (at < LCAP) sh.list[at] = l;
+        atomicAdd(&sh.cnt[par][b], 1u);
+        if (MASS) atomicAdd(&sh.mass[par][b], wt(x));
       }
       __syncwarp();
     }
@@ -370,57 +384,45 @@ template <bool RES, int NT> struct Sampler {
       });
     }
   }
-  // The last place that stays: in the order of the candidates lo .. hi (n of them), with `base`
-  // of the measure (their number, or with MASS their weight) before them, the one at which the
-  // running measure reaches `want`.  False: it is not reached.  The candidates are narrowed by
-  // RB at a time.
-  template <bool MASS>
-  __device__ bool resolve(int ph, bool all, const Cut& in, u64 lo, u64 hi, u64 n, u64 base, u64 want, u64& place) {
-    bool first = true;
-    while (n > 32 || first) {
-      if (n <= 32 && !all) break;
-      first = false;
-      const int par = level++ & 1;   // the other half may still be read by the cluster
-      for (int i = threadIdx.x; i < RB; i += NT) sh.mass[par][i] = 0, sh.cnt[par][i] = 0;
-      __syncthreads();
-      const int s = max(0, 64 - __clzll((long long)(hi - lo)) - 8);
-      candidates(ph, all, in, lo, hi, [&](float x, u64 pl) {
-        const int b = (int)((hi - pl) >> s);
-        atomicAdd(&sh.cnt[par][b], 1u);
-        if (MASS) atomicAdd(&sh.mass[par][b], wt(x));
-      });
-      cl.sync();
-      u64 c = 0, m = 0;
-      if (threadIdx.x < RB) {
-        uint32_t hc[CMAX];
-        u64 hm[CMAX];
+  // The bin of refinement `par` in which the running measure (number, or with MASS weight; `base`
+  // before the first bin) reaches `want`, into sh.ib[0], with the measure before it and the number
+  // of candidates in it in sh.bc.  False: it is not reached.
+  template <bool MASS> __device__ __forceinline__ bool reach(int par, u64 base, u64 want) {
+    u64 c[2] = {0, 0}, m[2] = {0, 0};
+    if (threadIdx.x < RB / 2) {
+      uint2 hc[CMAX];
+      ulonglong2 hm[CMAX];
 #pragma unroll
-        for (int r = 0; r < CMAX; ++r) {
-          hc[r] = r < C ? cl.map_shared_rank(&sh.cnt[par][0], r)[threadIdx.x] : 0;
-          hm[r] = MASS && r < C ? cl.map_shared_rank(&sh.mass[par][0], r)[threadIdx.x] : 0;
-        }
+      for (int r = 0; r < CMAX; ++r) {
+        hc[r] = r < C ? reinterpret_cast<const uint2*>(cl.map_shared_rank(&sh.cnt[par][0], r))[threadIdx.x] : make_uint2(0, 0);
+        hm[r] = MASS && r < C ? reinterpret_cast<const ulonglong2*>(cl.map_shared_rank(&sh.mass[par][0], r))[threadIdx.x]
+                              : make_ulonglong2(0, 0);
+      }
 #pragma unroll
-        for (int r = 0; r < CMAX; ++r) c += hc[r], m += hm[r];
-      }
-      if (!MASS) m = c;
-      u64 total;
-      const u64 incl = block_scan<NW>(m, sh.red, total);
-      if (base + total < want) return false;
-      if (base + incl - m < want && want <= base + incl) {
-        sh.ib[0] = threadIdx.x;
-        sh.bc[0] = base + incl - m;
-        sh.bc[1] = c;
-      }
-      __syncthreads();
-      const u64 b = sh.ib[0];
-      base = sh.bc[0];
-      n = sh.bc[1];
-      hi -= b << s;
-      const u64 span = (1ull << s) - 1;
-      if (hi - lo > span) lo = hi - span;
-      __syncthreads();
+      for (int r = 0; r < CMAX; ++r) c[0] += hc[r].x, c[1] += hc[r].y, m[0] += hm[r].x, m[1] += hm[r].y;
     }
-    candidates(ph, all, in, lo, hi, [&](float, u64 pl) {
+    if (!MASS) m[0] = c[0], m[1] = c[1];
+    u64 total;
+    u64 at = base + block_scan<NW>(m[0] + m[1], sh.red, total) - (m[0] + m[1]);
+    if (base + total < want) return false;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (at < want && want <= at + m[i]) {
+        sh.ib[0] = 2 * threadIdx.x + i;
+        sh.bc[0] = at;
+        sh.bc[1] = c[i];
+      }
+      at += m[i];
+    }
+    __syncthreads();
+    return true;
+  }
+  // The last place that stays among at most 32 candidates, those of phase ph that `is` holds:
+  // the one at which the running measure, `base` before them, reaches `want`.
+  template <bool MASS, typename F>
+  __device__ __forceinline__ bool rank_last(int ph, bool all, const Cut& in, u64 lo, u64 hi, F is, u64 base, u64 want, u64& place) {
+    candidates(ph, all, in, lo, hi, [&](float x, u64 pl) {
+      if (!is(x)) return;
       const uint32_t i = atomicAdd(&sh.gcnt[ph], 1u);
       if (i < 32) sh.glist[ph][i] = pl;
     });
@@ -450,24 +452,72 @@ template <bool RES, int NT> struct Sampler {
         if (opl > pl) before += ow;
       }
       u64 mine = pl && before < want ? pl : ~0ull;
-      u64 reach = pl ? before + w : 0;
+      u64 far = pl ? before + w : 0;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) {
         mine = min(mine, __shfl_xor_sync(0xffffffffu, mine, o));
-        reach = max(reach, __shfl_xor_sync(0xffffffffu, reach, o));
+        far = max(far, __shfl_xor_sync(0xffffffffu, far, o));
       }
-      if (threadIdx.x == 0) sh.bc[2] = reach >= want ? mine : 0;
+      if (threadIdx.x == 0) sh.bc[2] = far >= want ? mine : 0;
     }
     __syncthreads();
     place = sh.bc[2];
     return place != 0;
+  }
+  // The last place that stays: in the order of the candidates lo .. hi (n of them), with `base`
+  // of the measure before them, the one at which the running measure reaches `want`.  False: it
+  // is not reached.  The candidates are narrowed by RB at a time.
+  template <bool MASS>
+  __device__ bool resolve(int ph, bool all, const Cut& in, u64 lo, u64 hi, u64 n, u64 base, u64 want, u64& place) {
+    while (n > 32 || all) {
+      const int par = level++ & 1;   // the other half may still be read by the cluster
+      clear_level(par);
+      __syncthreads();
+      const int s = max(0, 64 - __clzll((long long)(hi - lo)) - 8);
+      candidates(ph, all, in, lo, hi, [&](float x, u64 pl) {
+        const int b = (int)((hi - pl) >> s);
+        atomicAdd(&sh.cnt[par][b], 1u);
+        if (MASS) atomicAdd(&sh.mass[par][b], wt(x));
+      });
+      cl.sync();
+      if (!reach<MASS>(par, base, want)) return false;
+      const u64 b = sh.ib[0];
+      base = sh.bc[0];
+      n = sh.bc[1];
+      hi -= b << s;
+      const u64 span = (1ull << s) - 1;
+      if (hi - lo > span) lo = hi - span;
+      __syncthreads();
+      if (n <= 32) break;
+    }
+    return rank_last<MASS>(ph, all, in, lo, hi, [](float) { return true; }, base, want, place);
+  }
+  // The same for the candidates that list_each4 has counted in refinement `par` (a cluster
+  // barrier after it): with at most 32 in the bin that reaches `want` they are ranked at once,
+  // else (many equal logits, a list that is full) narrowed by their places.
+  template <bool MASS>
+  __device__ bool settle(int ph, int par, const Steps& steps, const Cut& in, u64 base, u64 want, u64& place) {
+    u64 n, lo, hi;
+    bool all;
+    range(ph, n, lo, hi, all);
+    if (n == 0) return false;
+    if (!all) {
+      if (!reach<MASS>(par, base, want)) return false;
+      const int bin = sh.ib[0];
+      const u64 before = sh.bc[0], here = sh.bc[1];
+      __syncthreads();
+      if (here <= 32)
+        return rank_last<MASS>(ph, false, in, lo, hi, [&](float x) { return steps(wt, x) == bin; }, before, want, place);
+    }
+    return resolve<MASS>(ph, all, in, lo, hi, n, base, want, place);
   }
 };
 }  // namespace
 
 template <bool RES, int NT>
 __global__ void __launch_bounds__(NT, 1024 / NT) k_sample(SampleParams p, int chunk_quads) {
-  constexpr int NW = NT / 32, BPT = Sampler<RES, NT>::BPT;
+  constexpr int NW = NT / 32;
+  typedef typename Sampler<RES, NT>::Steps Steps;
   extern __shared__ __align__(16) float4 chunk[];
   __shared__ Shared sh;
   cg::cluster_group cl = cg::this_cluster();
@@ -551,18 +601,30 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_sample(SampleParams p, int ch
     // the row's k-th token is at least as likely: the candidates are the bins down to there.
     // With fewer than k threads' worth, or that bin too full, a histogram of the whole row is
     // taken and the candidates are the one bin in which it reaches k.
-    uint32_t c[BPT], own = 0, total;
-    u64 n, lo, hi, before = 0;
-    bool all = true;
+    uint32_t c[4], total;
+    u64 before = 0;
+    bool all = true;                                             // (a list is full)
     float blo = MAGIC, bhi = MAGIC;
+    int par = 0;
     if (float b = wt.bin(own_mx); b < MAGIC + BINS) atomicAdd(&sh.hist[bin_index(b)], 1u);
     cl.sync();
-    sm.counts(c);
+    // the bin in which the histogram reaches k, and how many are before it
+    auto reach_k = [&] {
+      sm.counts(c);
+      const uint32_t own = c[0] + c[1] + c[2] + c[3];
+      uint32_t n0 = block_scan<NW>(own, reinterpret_cast<uint32_t*>(sh.red), total) - own;
 #pragma unroll
-    for (int i = 0; i < BPT; ++i) own += c[i];
-    uint32_t n0 = block_scan<NW>(own, reinterpret_cast<uint32_t*>(sh.red), total) - own;
+      for (int i = 0; i < 4; ++i) {
+        if (n0 < (uint32_t)k && (uint32_t)k <= n0 + c[i]) sh.ib[0] = 4 * tid + i, sh.bc[0] = n0;
+        n0 += c[i];
+      }
+      __syncthreads();
+    };
     auto list = [&] {
-      sm.list_each4(0, [&](const float* x, int) {
+      par = sm.level++ & 1;
+      sm.clear_level(par);
+      __syncthreads();
+      sm.template list_each4<false>(0, par, Steps(blo, bhi), [&](const float* x, int) {
         uint32_t bits = 0;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -572,15 +634,10 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_sample(SampleParams p, int ch
         return bits;
       });
       cl.sync();
-      sm.range(0, n, lo, hi, all);
+      all = __any_sync(0xffffffffu, lane < C && *cl.map_shared_rank(&sh.fcnt[0], min(lane, C - 1)) > LCAP);
     };
+    reach_k();
     if (total >= (uint32_t)k) {
-#pragma unroll
-      for (int i = 0; i < BPT; ++i) {
-        if (n0 < (uint32_t)k && (uint32_t)k <= n0 + c[i]) sh.ib[0] = BPT * tid + i;
-        n0 += c[i];
-      }
-      __syncthreads();
       bhi = MAGIC + (float)sh.ib[0];
       list();
     }
@@ -595,19 +652,9 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_sample(SampleParams p, int ch
         if (b < MAGIC + BINS) atomicAdd(&sh.hist[bin_index(b)], 1u);
       });
       cl.sync();
-      sm.counts(c);
-      own = 0;
-#pragma unroll
-      for (int i = 0; i < BPT; ++i) own += c[i];
-      n0 = block_scan<NW>(own, reinterpret_cast<uint32_t*>(sh.red), total) - own;
+      reach_k();
       border = total > (uint32_t)k;                              // else every token that weighs something stays
       if (border) {
-#pragma unroll
-        for (int i = 0; i < BPT; ++i) {
-          if (n0 < (uint32_t)k && (uint32_t)k <= n0 + c[i]) sh.ib[0] = BPT * tid + i, sh.bc[0] = n0;
-          n0 += c[i];
-        }
-        __syncthreads();
         blo = bhi = MAGIC + (float)sh.ib[0];
         before = sh.bc[0];
         list();
@@ -617,7 +664,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_sample(SampleParams p, int ch
     }
     if (border) {
       const Cut in{bhi, 0};                                      // (the places leave only the candidates)
-      sm.template resolve<false>(0, all, in, lo, hi, n, before, (u64)k, cut.place);
+      sm.template settle<false>(0, par, Steps(blo, bhi), in, before, (u64)k, cut.place);
       cut.L = wt.bin(of_key((uint32_t)(cut.place >> IDX_BITS)));
     }
     if (top_p < 1.f) {
@@ -657,27 +704,31 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_sample(SampleParams p, int ch
     else count(std::false_type());
     if (tid < 2) sh.ib[2 + tid] = tid ? BINS - 1 : 0;
     cl.sync();
+    int par;
     {
       // the bins in which the running weight reaches the border less, and plus, the margin
-      uint32_t c[BPT];
-      u64 w[BPT], own = 0, all;
+      uint32_t c[4];
+      u64 w[4], own = 0, all;
       sm.counts(c);
 #pragma unroll
-      for (int i = 0; i < BPT; ++i) own += w[i] = (u64)((float)c[i] * exp2f(20.f - (float)(BPT * tid + i) / 16.f));
+      for (int i = 0; i < 4; ++i) own += w[i] = (u64)((float)c[i] * exp2f(20.f - (float)(4 * tid + i) / 16.f));
       u64 at = block_scan<NW>(own, sh.red, all) - own;
       const u64 b0 = (u64)fmax(0.0, ((double)top_p - 6e-4) * (double)all), b1 = (u64)(((double)top_p + 6e-4) * (double)all);
 #pragma unroll
-      for (int i = 0; i < BPT; ++i) {
-        if (at < b0 && b0 <= at + w[i]) sh.ib[2] = BPT * tid + i;
-        if (at < b1 && b1 <= at + w[i]) sh.ib[3] = BPT * tid + i;
+      for (int i = 0; i < 4; ++i) {
+        if (at < b0 && b0 <= at + w[i]) sh.ib[2] = 4 * tid + i;
+        if (at < b1 && b1 <= at + w[i]) sh.ib[3] = 4 * tid + i;
         at += w[i];
       }
+      par = sm.level++ & 1;
+      sm.clear_level(par);
       __syncthreads();
     }
     const float blo = MAGIC + (float)sh.ib[2], bhi = MAGIC + (float)sh.ib[3];
+    const Steps steps(blo, bhi);
     Sum sum_total, sum_above;
     auto weigh = [&](auto wide, auto with_cut) {
-      sm.list_each4(1, [&](const float* x, int l) {
+      sm.template list_each4<true>(1, par, steps, [&](const float* x, int l) {
         float b[4];
         uint32_t bits = 0;
         F2 f;
@@ -709,24 +760,18 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_sample(SampleParams p, int ch
     u64 total = warp_sum64(sum_total.units()), above = warp_sum64(sum_above.units());
     if (lane == 0) sh.wsum[warp] = above, sh.red[warp] = total;
     __syncthreads();
-    if (tid == 0) {
-      u64 t = 0, a = 0;
-#pragma unroll
-      for (int w = 0; w < NW; ++w) t += sh.red[w], a += sh.wsum[w];
-      sh.total = t;
-      sh.above = a;
+    if (warp == 0) {
+      const u64 t = warp_sum64(lane < NW ? sh.red[lane] : 0), a = warp_sum64(lane < NW ? sh.wsum[lane] : 0);
+      if (lane == 0) sh.total = t, sh.above = a;
     }
     cl.sync();
     total = warp_sum64(lane < C ? *cl.map_shared_rank(&sh.total, lane) : 0);
     above = warp_sum64(lane < C ? *cl.map_shared_rank(&sh.above, lane) : 0);
-    u64 n, lo, hi;
-    bool all;
-    sm.range(1, n, lo, hi, all);
     const u64 want = (u64)max(1.0, ceil((double)fmaxf(top_p, 0.f) * (double)total));
     u64 place = 0;
-    summed = above < want && n > 0 && !all;
-    bool ok = above < want && n > 0 &&
-              sm.template resolve<true>(1, all, cut, lo, hi, n, above, want, place);
+    const bool full = __any_sync(0xffffffffu, lane < C && *cl.map_shared_rank(&sh.fcnt[1], min(lane, C - 1)) > LCAP);
+    summed = above < want && !full;
+    const bool ok = above < want && sm.template settle<true>(1, par, steps, cut, above, want, place);
     if (!ok) {                                                   // the bracket missed the border: the whole order
       cl.sync();
       if (tid == 0) sh.gcnt[1] = 0;
