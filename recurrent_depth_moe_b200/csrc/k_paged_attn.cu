@@ -955,7 +955,8 @@ bool mma_takes(int dtype, const PagedView& c) {
   return dtype == 1 && c.hd % 8 == 0 && rb % 16 == 0 && !(((uintptr_t)c.k | (uintptr_t)c.v) & 15);
 }
 int ctas_mma(bool e4m3) { return device_sm_count() * (e4m3 ? Tile<true>::CTAS : Tile<false>::CTAS); }
-int ctas_simt() { return device_sm_count() * 3; }   // (an fp32 tile of 128 channels, twice, is 68 KB)
+constexpr int SIMT_CTAS = 3;   // on an SM at most: registers (an fp32 tile of 128 channels, twice, is 68 KB)
+int ctas_simt(int smem) { return device_sm_count() * std::max(1, std::min(SIMT_CTAS, 227 * 1024 / (smem + 4096))); }
 // descriptors, then the parts of `ctas` CTAs and, on tensor cores, of their warps
 size_t scratch_bytes(int ctas, int parts, int hd) {
   return (size_t)ctas * sizeof(Desc) + (size_t)parts * 2 * GT * (hd + 2) * sizeof(float);
@@ -981,7 +982,7 @@ template <typename T> int launch_join(const PagedAttnParams& p, int ctas, cudaSt
 // The same for every batch and head count: the parts belong to the CTAs.
 size_t paged_attn_scratch(const PagedView& c) {
   const int n = ctas_mma(c.e4m3);
-  return std::max(scratch_bytes(n, n * (1 + WARPS), c.hd), scratch_bytes(ctas_simt(), ctas_simt(), c.hd));
+  return std::max(scratch_bytes(n, n * (1 + WARPS), c.hd), scratch_bytes(ctas_simt(0), ctas_simt(0), c.hd));
 }
 
 int launch_paged_attn(int dtype, const PagedAttnParams& p0, cudaStream_t s) {
@@ -990,7 +991,10 @@ int launch_paged_attn(int dtype, const PagedAttnParams& p0, cudaStream_t s) {
   p.ps_shift = -1;
   for (int i = 0; i < 31; ++i)
     if (p.c.page_size == 1 << i) p.ps_shift = i;
-  const int ctas = tc ? ctas_mma(p.c.e4m3) : ctas_simt();
+  const int eb = p.c.e4m3 ? 1 : dtype == 0 ? 4 : 2, G = p.H / p.c.Hkv;
+  const bool vec = p.c.hd % 4 == 0 && !(((uintptr_t)p.c.k | (uintptr_t)p.c.v) & (4 * eb - 1));
+  const int nh = G >= 5 ? 8 : G >= 3 ? 4 : G, buffers = vec && dtype == 0 && !p.c.e4m3 ? 2 : 1;
+  const int simt_smem = (int)PlainSm::bytes(p.c.hd, nh, buffers), ctas = tc ? ctas_mma(p.c.e4m3) : ctas_simt(simt_smem);
   p.part_ml = reinterpret_cast<float*>((char*)p.scratch + (size_t)ctas * sizeof(Desc));
   p.part_o = p.part_ml + (size_t)(tc ? ctas * (1 + WARPS) : ctas) * 2 * GT * 2;
   if (tc) {
@@ -1014,10 +1018,7 @@ int launch_paged_attn(int dtype, const PagedAttnParams& p0, cudaStream_t s) {
     note_launch();
     return launch_join<bf16>(p, ctas, s);
   }
-  const int eb = p.c.e4m3 ? 1 : dtype == 0 ? 4 : 2, G = p.H / p.c.Hkv;
-  const bool vec = p.c.hd % 4 == 0 && !(((uintptr_t)p.c.k | (uintptr_t)p.c.v) & (4 * eb - 1));
-  const int nh = G >= 5 ? 8 : G >= 3 ? 4 : G, buffers = vec && dtype == 0 && !p.c.e4m3 ? 2 : 1;
-  const int smem = (int)PlainSm::bytes(p.c.hd, nh, buffers), most = (int)PlainSm::bytes(256, 8, 2);
+  const int most = (int)PlainSm::bytes(256, 8, 2);
   void (*kernel)(PagedAttnParams, int) = nullptr;
 #define RDT_SIMT(TT, QQ, NN) kernel = vec ? k_paged_attn_simt<TT, QQ, NN, true> : k_paged_attn_simt<TT, QQ, NN, false>
 #define RDT_SIMT_H(TT, QQ)              \
@@ -1037,7 +1038,7 @@ int launch_paged_attn(int dtype, const PagedAttnParams& p0, cudaStream_t s) {
 #undef RDT_SIMT_H
 #undef RDT_SIMT
   if (!ensure_smem_limit((const void*)kernel, most)) return -1;
-  kernel<<<ctas, 128, smem, s>>>(p, 3);
+  kernel<<<ctas, 128, simt_smem, s>>>(p, 3);
   note_launch();
   return dtype == 0 ? launch_join<float>(p, ctas, s) : launch_join<bf16>(p, ctas, s);
 }

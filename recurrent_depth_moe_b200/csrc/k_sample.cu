@@ -39,7 +39,8 @@ constexpr int NWMAX = 16;        // warps of a CTA
 constexpr int BINS = 46 * 16;    // of the exponent: below 2^-46 a weight rounds to nothing
 constexpr int RB = 256;          // bins of one refinement
 constexpr int HB = BINS / 4;     // threads that sum the cluster's histograms, four bins each
-constexpr int LCAP = 1024;       // candidates one CTA lists; more are found by passes over the row
+constexpr int LCAP = 1000;       // candidates one CTA lists (below 2^10: sums of their weights' halves stay in 32
+                                 // bits); more are found by passes over the row
 constexpr int IDX_BITS = 20;
 constexpr int CMAX = 8;          // CTAs of a cluster
 typedef unsigned long long u64;
@@ -192,6 +193,11 @@ template <typename V> __device__ __forceinline__ V warp_scan(V v) {   // inclusi
   }
   return v;
 }
+// A barrier of the cluster, with its shared memory visible across it; of one CTA, the CTA's.
+__device__ __forceinline__ void cluster_sync(const cg::cluster_group& cl, int C) {
+  if (C > 1) cl.sync();
+  else __syncthreads();
+}
 // Inclusive sum over the block's NW warps; `red` holds NW values, `total` the block's.
 template <int NW, typename V> __device__ __forceinline__ V block_scan(V v, V* red, V& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -299,7 +305,9 @@ template <bool RES, int NT> struct Sampler {
     __device__ __forceinline__ Steps(float blo, float bhi)
         : lo(blo - Weigh::MAGIC - 0.5f), per((float)RB / (bhi - blo + 1.f)) {}
     __device__ __forceinline__ int operator()(const Weigh& wt, float x) const {
-      return min(RB - 1, max(0, __float2int_rd(((wt.m - x) * wt.c16 - lo) * per)));
+      // (no contraction: the same bin wherever this is inlined)
+      const float t = __fmul_rn(__fsub_rn(__fmul_rn(__fsub_rn(wt.m, x), wt.c16), lo), per);
+      return min(RB - 1, max(0, __float2int_rd(t)));
     }
   };
   __device__ __forceinline__ void clear_level(int par) {
@@ -426,7 +434,7 @@ template <bool RES, int NT> struct Sampler {
       const uint32_t i = atomicAdd(&sh.gcnt[ph], 1u);
       if (i < 32) sh.glist[ph][i] = pl;
     });
-    cl.sync();
+    cluster_sync(cl, C);
     if (threadIdx.x < 32) {
       // (places are not 0: the unused entries)
       const int lane = threadIdx.x;
@@ -479,7 +487,7 @@ template <bool RES, int NT> struct Sampler {
         atomicAdd(&sh.cnt[par][b], 1u);
         if (MASS) atomicAdd(&sh.mass[par][b], wt(x));
       });
-      cl.sync();
+      cluster_sync(cl, C);
       if (!reach<MASS>(par, base, want)) return false;
       const u64 b = sh.ib[0];
       base = sh.bc[0];
@@ -564,7 +572,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_sample(SampleParams p, int ch
     mx = warp_max(lane < NW ? sh.fred[lane] : -INFINITY);
     if (lane == 0) sh.mx = mx;
   }
-  cl.sync();
+  cluster_sync(cl, C);
   mx = warp_max(lane < C ? *cl.map_shared_rank(&sh.mx, lane) : -INFINITY);
   if (!(T > 0.f) || mx == -INFINITY) {                           // the most likely token
     uint32_t best = 0x7fffffff;
@@ -573,13 +581,13 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_sample(SampleParams p, int ch
         best = min(best, (uint32_t)row.index(l + (x[0] == mx ? 0 : x[1] == mx ? 1 : x[2] == mx ? 2 : 3)));
     });
     if (best != 0x7fffffff) atomicMin(&sh.idx, best);
-    cl.sync();
+    cluster_sync(cl, C);
     if (rank == 0 && tid == 0) {
       for (int i = 0; i < C; ++i) best = min(best, *cl.map_shared_rank(&sh.idx, i));
       p.tokens[(long long)r * p.out_ld] = best == 0x7fffffff ? 0 : (int)best;
       if (p.logprob) p.logprob[r] = 0.f;
     }
-    cl.sync();                                                   // remote shared memory is read until here
+    cluster_sync(cl, C);                                                   // remote shared memory is read until here
     return;
   }
   if (mx == INFINITY) {
@@ -607,7 +615,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_sample(SampleParams p, int ch
     float blo = MAGIC, bhi = MAGIC;
     int par = 0;
     if (float b = wt.bin(own_mx); b < MAGIC + BINS) atomicAdd(&sh.hist[bin_index(b)], 1u);
-    cl.sync();
+    cluster_sync(cl, C);
     // the bin in which the histogram reaches k, and how many are before it
     auto reach_k = [&] {
       sm.counts(c);
@@ -633,7 +641,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_sample(SampleParams p, int ch
         }
         return bits;
       });
-      cl.sync();
+      cluster_sync(cl, C);
       all = __any_sync(0xffffffffu, lane < C && *cl.map_shared_rank(&sh.fcnt[0], min(lane, C - 1)) > LCAP);
     };
     reach_k();
@@ -643,7 +651,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_sample(SampleParams p, int ch
     }
     bool border = true;
     if (all) {
-      cl.sync();
+      cluster_sync(cl, C);
       for (int i = tid; i < BINS; i += NT) sh.hist[i] = 0;
       if (tid == 0) sh.fcnt[0] = sh.kmax[0] = 0, sh.kmin[0] = ~0u;
       __syncthreads();
@@ -651,7 +659,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_sample(SampleParams p, int ch
         const float b = wt.bin(x);
         if (b < MAGIC + BINS) atomicAdd(&sh.hist[bin_index(b)], 1u);
       });
-      cl.sync();
+      cluster_sync(cl, C);
       reach_k();
       border = total > (uint32_t)k;                              // else every token that weighs something stays
       if (border) {
@@ -659,7 +667,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_sample(SampleParams p, int ch
         before = sh.bc[0];
         list();
       } else {
-        cl.sync();
+        cluster_sync(cl, C);
       }
     }
     if (border) {
@@ -674,9 +682,9 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_sample(SampleParams p, int ch
   }
   bool summed = false;                                           // sh.wsum holds the kept weight
   if (top_p < 1.f) {
-    // A weight is counted as 12 bits of 2^-(bin / 16), interpolated linearly in the bin (up to
-    // half a bin to each side): off by less than 4e-4 of it, so bins whose running weight is
-    // within 6e-4 of the border bracket it.  (Tokens below 1e-4 / V of the largest weight hold
+    // A weight is counted as 11 bits of 2^-(bin / 16) (2^20 of them fit 32 bits), interpolated
+    // linearly in the bin (up to half a bin to each side): off by less than 5e-4 of it, so bins
+    // whose running weight is within 6e-4 of the border bracket it.  (Tokens below 1e-4 / V of the largest weight hold
     // less than 1e-4 of the total: they are not counted.)
     const float lim = fminf(MAGIC + (BINS - 1), cut.L);
     const bool cut_any = cut.L < MAGIC + BINS;
@@ -689,7 +697,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_sample(SampleParams p, int ch
           float b[2], v[2];
           F2 f;
           wt.bin2(x[e], x[e + 1], b[0], b[1], f);
-          fma2(f, F2(-177.45f), F2(4096.f + 8388608.f)).get(v[0], v[1]);
+          fma2(f, F2(-88.72f), F2(2048.f + 8388608.f)).get(v[0], v[1]);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             if (decltype(with_cut)::value && !cut.holds(b[i], x[e + i], row.index(l + e + i))) b[i] = MAGIC + BINS;
@@ -703,7 +711,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_sample(SampleParams p, int ch
     if (cut_any) count(std::true_type());
     else count(std::false_type());
     if (tid < 2) sh.ib[2 + tid] = tid ? BINS - 1 : 0;
-    cl.sync();
+    cluster_sync(cl, C);
     int par;
     {
       // the bins in which the running weight reaches the border less, and plus, the margin
@@ -764,7 +772,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_sample(SampleParams p, int ch
       const u64 t = warp_sum64(lane < NW ? sh.red[lane] : 0), a = warp_sum64(lane < NW ? sh.wsum[lane] : 0);
       if (lane == 0) sh.total = t, sh.above = a;
     }
-    cl.sync();
+    cluster_sync(cl, C);
     total = warp_sum64(lane < C ? *cl.map_shared_rank(&sh.total, lane) : 0);
     above = warp_sum64(lane < C ? *cl.map_shared_rank(&sh.above, lane) : 0);
     const u64 want = (u64)max(1.0, ceil((double)fmaxf(top_p, 0.f) * (double)total));
@@ -773,7 +781,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_sample(SampleParams p, int ch
     summed = above < want && !full;
     const bool ok = above < want && sm.template settle<true>(1, par, steps, cut, above, want, place);
     if (!ok) {                                                   // the bracket missed the border: the whole order
-      cl.sync();
+      cluster_sync(cl, C);
       if (tid == 0) sh.gcnt[1] = 0;
       if (tid < 32) sh.glist[1][tid] = 0;
       summed = false;
@@ -831,11 +839,11 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_sample(SampleParams p, int ch
     __syncthreads();
     if (lane == 0) sh.wsum[warp] = mine;
   }
-  cl.sync();
+  cluster_sync(cl, C);
   const u64 mine = tid < C * NW ? cl.map_shared_rank(&sh.wsum[0], tid / NW)[tid % NW] : 0;
   u64 total;
   const u64 incl = block_scan<NW>(mine, sh.red, total);
-  cl.barrier_arrive();                                           // the last read of remote shared memory is done
+  if (C > 1) cl.barrier_arrive();                                // the last read of remote shared memory is done
   const float u = p.u[r];
   const double uc = u > 0.f ? fmin((double)u, 1.0 - 0x1p-24) : 0.0;   // NaN: 0
   const u64 target = (u64)(uc * (double)total);
@@ -891,7 +899,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_sample(SampleParams p, int ch
       }
     }
   }
-  cl.barrier_wait();
+  if (C > 1) cl.barrier_wait();
 }
 
 // Cluster size: two CTAs on an SM can hold 100 KB of a row each, so that one's passes run while

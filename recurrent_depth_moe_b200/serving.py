@@ -17,6 +17,7 @@ from . import _native as N
 _DT = {"fp32": (0, torch.float32), "bf16": (1, torch.bfloat16)}
 _NAME = {torch.float32: "fp32", torch.bfloat16: "bf16"}
 E4M3 = torch.float8_e4m3fn
+_PARAMS = ("temperature", "top_k", "top_p", "min_p")
 
 
 def _lib():
@@ -244,25 +245,31 @@ def sample_tokens(logits: torch.Tensor, u: torch.Tensor, temperature: Union[floa
     token.  Returns int32 [n], with return_logprob also the drawn tokens' log-probabilities
     among the kept tokens (fp32 [n])."""
     if not isinstance(logits, torch.Tensor) or not logits.is_cuda or logits.dtype != torch.float32 or \
-            logits.dim() != 2 or logits.shape[1] < 1 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+            logits.dim() != 2 or logits.shape[1] < 1:
         raise ValueError("logits: expected a CUDA float32 [n, vocab] tensor with contiguous rows")
     n, V = logits.shape
     dev = logits.device
-    ld = logits.stride(0) if n > 1 else V
-    if ld < V:
-        raise ValueError("logits: the rows must not overlap")
-    _check(u, "u", torch.float32, (n,), dev)
-    a = N.rdt_sampling(1.0, 0, 1.0, 0.0)
-    for name, val, dt in (("temperature", temperature, torch.float32), ("top_k", top_k, torch.int32),
-                          ("top_p", top_p, torch.float32), ("min_p", min_p, torch.float32)):
+    ld = V
+    if not logits.is_contiguous():
+        if V > 1 and logits.stride(1) != 1:
+            raise ValueError("logits: expected a CUDA float32 [n, vocab] tensor with contiguous rows")
+        ld = logits.stride(0) if n > 1 else V
+        if ld < V:
+            raise ValueError("logits: the rows must not overlap")
+    shape = (n,)
+    _check(u, "u", torch.float32, shape, dev)
+    scalars, rows = [1.0, 0, 1.0, 0.0], [None] * 4
+    for i, (val, name) in enumerate(zip((temperature, top_k, top_p, min_p), _PARAMS)):
         if isinstance(val, torch.Tensor):
-            _check(val, name, dt, (n,), dev)
-            setattr(a, name + "_rows", val.data_ptr())
+            _check(val, name, torch.int32 if i == 1 else torch.float32, shape, dev)
+            rows[i] = val.data_ptr()
         else:
-            setattr(a, name, val)
+            scalars[i] = val
+    a = N.rdt_sampling(*scalars, *rows)
     if out is None:
         out = torch.empty(n, dtype=torch.int32, device=dev)
-    elif out.device != dev or out.dtype != torch.int32 or tuple(out.shape) != (n,) or (n > 1 and out.stride(0) < 1):
+    elif not isinstance(out, torch.Tensor) or out.device != dev or out.dtype != torch.int32 or out.shape != shape or \
+            (n > 1 and out.stride(0) < 1):
         raise ValueError(f"out: expected int32 ({n},) on {dev}")
     lp = torch.empty(n, dtype=torch.float32, device=dev) if return_logprob else None
     _call("rdt_sample_tokens", dev, logits.data_ptr(), ld, n, V, u.data_ptr(), ctypes.byref(a), out.data_ptr(),
