@@ -604,6 +604,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_sample(SampleParams p, int ch
   Sampler<RES, NT> sm(sh, row, wt);
   constexpr float MAGIC = Weigh::MAGIC;
   Cut cut{MAGIC + BINS, 0};
+  bool listed = false;                                           // every token in play is in a list, in these steps:
+  Steps listed_steps(MAGIC, MAGIC);
   if (k > 0 && k < p.vocab) {
     // The largest element of each thread is a subset of the row, so where k of those are reached
     // the row's k-th token is at least as likely: the candidates are the bins down to there.
@@ -672,16 +674,53 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_sample(SampleParams p, int ch
     }
     if (border) {
       const Cut in{bhi, 0};                                      // (the places leave only the candidates)
-      sm.template settle<false>(0, par, Steps(blo, bhi), in, before, (u64)k, cut.place);
+      listed = sm.template settle<false>(0, par, Steps(blo, bhi), in, before, (u64)k, cut.place) && blo == MAGIC && !all;
+      listed_steps = Steps(blo, bhi);
       cut.L = wt.bin(of_key((uint32_t)(cut.place >> IDX_BITS)));
     }
-    if (top_p < 1.f) {
+    if (top_p < 1.f && !listed) {
       for (int i = tid; i < BINS; i += NT) sh.hist[i] = 0;
       __syncthreads();
     }
   }
   bool summed = false;                                           // sh.wsum holds the kept weight
-  if (top_p < 1.f) {
+  if (top_p < 1.f && listed) {
+    // what top-k left is few: its weights are counted from the lists
+    const int par = sm.level++ & 1;
+    sm.clear_level(par);
+    if (tid == 0) sh.fcnt[1] = sh.fcnt[0];
+    __syncthreads();
+    const u64 top = (1ull << (32 + IDX_BITS)) - 1;
+    u64 total = 0;
+    sm.candidates(1, false, cut, cut.place, top, [&](float x, u64) {
+      const u64 w = wt(x);
+      const int b = listed_steps(wt, x);
+      atomicAdd(&sh.cnt[par][b], 1u);
+      atomicAdd(&sh.mass[par][b], w);
+      total += w;
+    });
+    total = warp_sum64(total);
+    if (lane == 0) sh.red[warp] = total;
+    __syncthreads();
+    if (warp == 0) {
+      total = warp_sum64(lane < NW ? sh.red[lane] : 0);
+      if (lane == 0) sh.total = total;
+    }
+    cluster_sync(cl, C);
+    total = warp_sum64(lane < C ? *cl.map_shared_rank(&sh.total, lane) : 0);
+    const u64 want = (u64)max(1.0, ceil((double)fmaxf(top_p, 0.f) * (double)total));
+    sm.template reach<true>(par, 0, want);                       // (the total is the bins' own)
+    const int bin = sh.ib[0];
+    const u64 before = sh.bc[0], here = sh.bc[1];
+    __syncthreads();
+    u64 place = 0;
+    if (here <= 32)
+      sm.template rank_last<true>(1, false, cut, cut.place, top, [&](float x) { return listed_steps(wt, x) == bin; }, before,
+                                  want, place);
+    else
+      sm.template resolve<true>(1, false, cut, cut.place, top, (u64)p.vocab, 0, want, place);
+    cut.place = place;
+  } else if (top_p < 1.f) {
     // A weight is counted as 11 bits of 2^-(bin / 16) (2^20 of them fit 32 bits), interpolated
     // linearly in the bin (up to half a bin to each side): off by less than 5e-4 of it, so bins
     // whose running weight is within 6e-4 of the border bracket it.  (Tokens below 1e-4 / V of the largest weight hold
@@ -802,10 +841,12 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_sample(SampleParams p, int ch
   // beyond x >= xlim: a token level with the border
   auto drops = [&](float x, int l) { return by_place && x == xcut && place_of(x, row.index(l)) < cut.place; };
   auto kept = [&](float x, int l) -> u64 { return x >= xlim && !drops(x, l) ? wt(x) : 0; };
-  if (summed && xmin <= xcut) {
-    // the weight before the bracket is known: the kept candidates join their pieces
-    // (22 bits to a word: up to LCAP of them fit)
-    for (uint32_t i = tid; i < sh.fcnt[1]; i += NT) {
+  if (listed || (summed && xmin <= xcut)) {
+    // the weight before the bracket is known (with a list of all: none): the kept candidates
+    // join their pieces (22 bits to a word: up to LCAP of them fit)
+    if (listed && tid < NW) sh.wsum[tid] = 0;
+    const uint32_t n = listed ? sh.fcnt[0] : sh.fcnt[1];
+    for (uint32_t i = tid; i < n; i += NT) {
       const int l = sh.list[i], w = (l >> 2) / piece;
       const u64 q = kept(row.at(l), l);
       if (q) atomicAdd(&sh.add[w][0], (uint32_t)q & 0x3fffffu), atomicAdd(&sh.add[w][1], (uint32_t)(q >> 22));
