@@ -136,12 +136,14 @@ namespace {
 // for memory, so it takes the deeper ring (105 us against 110 with 2 and 3, one sequence of
 // 131,071 keys); e4m3 issues twice the instructions a byte and takes more warps (313 us against
 // 342, 128 sequences of 4097 to 8191 keys).
-template <bool Q> struct Tile { static constexpr int KEYS = Q ? 32 : 16, STAGES = Q ? 2 : 3, CTAS = Q ? 3 : 2; };
+template <int HD, bool Q> struct Tile {
+  static constexpr int KEYS = Q || HD == 64 ? 32 : 16, STAGES = Q ? 2 : 3, CTAS = Q ? 3 : 2;
+};
 
 template <int HD, bool Q> struct Ring {    // HD: the head width rounded up to 64, 128 or 256
   static constexpr int ROW = HD * (Q ? 1 : 2);                  // bytes of a row
-  static constexpr int STAGE = 2 * Tile<Q>::KEYS * ROW;         // K then V
-  static constexpr int BYTES = Tile<Q>::STAGES * STAGE;         // of a warp
+  static constexpr int STAGE = 2 * Tile<HD, Q>::KEYS * ROW;         // K then V
+  static constexpr int BYTES = Tile<HD, Q>::STAGES * STAGE;         // of a warp
 };
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
@@ -205,8 +207,8 @@ template <int PIECES> __device__ __forceinline__ int swz_v(int r, int c) {
 __device__ __forceinline__ float pow2_down(int d) { return d < -126 ? 0.f : __int_as_float((127 + d) << 23); }
 
 template <int HD, bool Q, bool UNI>
-__global__ void __launch_bounds__(32 * WARPS, HD <= 128 ? Tile<Q>::CTAS : 1) k_paged_attn_mma(PagedAttnParams p, int least) {
-  constexpr int KEYS = Tile<Q>::KEYS, STAGES = Tile<Q>::STAGES, ROW = Ring<HD, Q>::ROW, STAGE = Ring<HD, Q>::STAGE;
+__global__ void __launch_bounds__(32 * WARPS, HD <= 128 ? Tile<HD, Q>::CTAS : 1) k_paged_attn_mma(PagedAttnParams p, int least) {
+  constexpr int KEYS = Tile<HD, Q>::KEYS, STAGES = Tile<HD, Q>::STAGES, ROW = Ring<HD, Q>::ROW, STAGE = Ring<HD, Q>::STAGE;
   constexpr int NG = KEYS / 8;                        // groups of 8 keys
   constexpr unsigned ALL = KEYS == 32 ? 0xffffffffu : (1u << KEYS % 32) - 1;
   constexpr int PIECES = ROW / 16, EPP = Q ? 16 : 8;  // 16-byte pieces of a row, elements of a piece
@@ -954,7 +956,7 @@ bool mma_takes(int dtype, const PagedView& c) {
   const int rb = c.hd * (c.e4m3 ? 1 : 2);
   return dtype == 1 && c.hd % 8 == 0 && rb % 16 == 0 && !(((uintptr_t)c.k | (uintptr_t)c.v) & 15);
 }
-int ctas_mma(bool e4m3) { return device_sm_count() * (e4m3 ? Tile<true>::CTAS : Tile<false>::CTAS); }
+int ctas_mma(bool e4m3) { return device_sm_count() * (e4m3 ? Tile<128, true>::CTAS : Tile<128, false>::CTAS); }
 constexpr int SIMT_CTAS = 3;   // on an SM at most: registers (an fp32 tile of 128 channels, twice, is 68 KB)
 int ctas_simt(int smem) { return device_sm_count() * std::max(1, std::min(SIMT_CTAS, 227 * 1024 / (smem + 4096))); }
 // descriptors, then the parts of `ctas` CTAs and, on tensor cores, of their warps
