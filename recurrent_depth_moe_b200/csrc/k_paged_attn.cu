@@ -597,15 +597,20 @@ __global__ void __launch_bounds__(32 * WARPS, HD <= 128 ? Tile<HD, Q>::CTAS : 1)
       const int part = lane < 2 * WARPS && lane >= i && lane <= last && run_id[lane] == id ? lane : -1;
       const float2 ml = part >= 0 ? *reinterpret_cast<const float2*>(part_ml(p, first + (part >> 1), part & 1) + h * 2)
                                   : make_float2(-INFINITY, 0.f);
-      const float M = warp_max(ml.x), base = M == -INFINITY ? 0.f : M;
-      const float w = ex2(ml.x - base), L = warp_sum(w * ml.y), inv = begun && ended ? (L != 0.f ? 1.f / L : 0.f) : 1.f;
       const unsigned parts = __ballot_sync(0xffffffffu, part >= 0);
-      for (int ch = 4 * lane; ch < (hd + 127) / 128 * 128; ch += 128) {
-        float4 v[2 * WARPS], o = make_float4(0.f, 0.f, 0.f, 0.f);
+      float4 v[2 * WARPS];
+      auto load = [&](int ch) {                       // (the first before m and l are in)
 #pragma unroll
         for (int k = 0; k < 2 * WARPS; ++k)
           if ((parts >> k & 1) && ch < hd)
             v[k] = *reinterpret_cast<const float4*>(part_o(p, first + (k >> 1), k & 1) + h * hd + ch);
+      };
+      load(4 * lane);
+      const float M = warp_max(ml.x), base = M == -INFINITY ? 0.f : M;
+      const float w = ex2(ml.x - base), L = warp_sum(w * ml.y), inv = begun && ended ? (L != 0.f ? 1.f / L : 0.f) : 1.f;
+      for (int ch = 4 * lane; ch < (hd + 127) / 128 * 128; ch += 128) {
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (ch >= 128) load(ch);
 #pragma unroll
         for (int k = 0; k < 2 * WARPS; ++k) {
           const float wk = __shfl_sync(0xffffffffu, w, k);
@@ -901,30 +906,49 @@ __global__ void __launch_bounds__(128) k_paged_attn_join(PagedAttnParams p) {
   if (h >= min(GT, G - h0)) return;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   // part 1 of the first CTA, part 0 of the others
-  float M = -INFINITY, L = 0.f;
-  for (int s = tid; s < n; s += 128) M = fmaxf(M, part_ml(p, d.first + s, s == 0)[h * 2]);
+  const bool by4 = hd % 4 == 0;
+  float4 ahead[8];                                    // a warp's first parts, loaded before their weights are known
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int s = warp + i * WARPS;
+    ahead[i] = by4 && s < n && 4 * lane < hd
+                   ? *reinterpret_cast<const float4*>(part_o(p, d.first + s, s == 0) + h * hd + 4 * lane)
+                   : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  const float2 none = make_float2(-INFINITY, 0.f);
+  const float2 ml0 = tid < n ? *reinterpret_cast<const float2*>(part_ml(p, d.first + tid, tid == 0) + h * 2) : none;
+  float M = ml0.x, L = 0.f;
+  for (int s = tid + 128; s < n; s += 128) M = fmaxf(M, part_ml(p, d.first + s, 0)[h * 2]);
   M = warp_max(M);
   if (lane == 0) red[warp] = M;
   __syncthreads();
   M = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
   const float base = M == -INFINITY ? 0.f : M;
   for (int s = tid; s < n; s += 128) {
-    const float* ml = part_ml(p, d.first + s, s == 0);
-    const float w = exp2f(ml[h * 2] - base);
+    const float2 ml = s == tid ? ml0 : *reinterpret_cast<const float2*>(part_ml(p, d.first + s, 0) + h * 2);
+    const float w = exp2f(ml.x - base);
     wj[s] = w;
-    L += w * ml[h * 2 + 1];
+    L += w * ml.y;
   }
   __syncthreads();
   L = block_sum(L, red);
   const float inv = L != 0.f ? 1.f / L : 0.f;
   T* o = (T*)p.o + (long long)d.b * p.o_row + (long long)(g * G + h0 + h) * hd;
-  if (hd % 4 == 0) {
+  if (by4) {
     for (int ch0 = 0; ch0 < hd; ch0 += 128) {
       const int ch = ch0 + 4 * lane;
       float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
       if (ch < hd) {
+        int s = warp;
+        if (ch0 == 0)
+#pragma unroll
+          for (int i = 0; i < 8; ++i, s += WARPS) {
+            const float w = s < n ? wj[s] : 0.f;
+            a.x = fmaf(w, ahead[i].x, a.x); a.y = fmaf(w, ahead[i].y, a.y);
+            a.z = fmaf(w, ahead[i].z, a.z); a.w = fmaf(w, ahead[i].w, a.w);
+          }
 #pragma unroll 8
-        for (int s = warp; s < n; s += WARPS) {
+        for (; s < n; s += WARPS) {
           const float4 x = *reinterpret_cast<const float4*>(part_o(p, d.first + s, s == 0) + h * hd + ch);
           const float w = wj[s];
           a.x = fmaf(w, x.x, a.x); a.y = fmaf(w, x.y, a.y); a.z = fmaf(w, x.z, a.z); a.w = fmaf(w, x.w, a.w);
