@@ -129,6 +129,24 @@ def check_attention(cache, q, lens, out, scale=None, loop=0, half_weights=None):
     return worst
 
 
+def sample_interval(x, tok, T=1.0, k=0, p=1.0, m=0.0):
+    """The share of the kept weight before token tok and up to it, over the tokens that
+    sample_row's definition keeps (tok itself joins them if it is not one)."""
+    x = x.detach().cpu().double()
+    val, idx = torch.sort(x, descending=True, stable=True)
+    w = torch.exp((val - val[0]) / T)
+    keep = torch.arange(len(x)) < (k or len(x))
+    w = torch.where(keep, w, torch.zeros((), dtype=F64))
+    if p < 1:
+        keep &= torch.cumsum(w, 0) - w < p * w.sum()
+    if m > 0:
+        keep &= (val - val[0]) / T >= math.log(m)
+    full = torch.zeros_like(w).scatter_(0, idx, torch.where(keep, w, torch.zeros((), dtype=F64)))
+    full[tok] = math.exp((float(x[tok]) - float(val[0])) / T)
+    c = torch.cumsum(full, 0) / full.sum()
+    return float(c[tok] - full[tok] / full.sum()), float(c[tok])
+
+
 def sample_row(x, u, T=1.0, k=0, p=1.0, m=0.0):
     """The sampled token of one row, from the definition in 64 bits: (token, logprob, margin),
     margin the smallest relative distance of u and of top-p's border to the running sums that

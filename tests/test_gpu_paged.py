@@ -382,3 +382,80 @@ def test_empty_calls():
     k, _ = R.paged_kv_read(_i32([]), cache, t_out=4)
     assert k.shape == (0, 1, 4, 32)
     assert R.paged_kv_read(_i32([1, 1]), cache, t_out=0)[0].shape == (2, 1, 0, 32)
+
+
+MORE = [  # dtype, H, Hkv, hd, page, lens: every head count of the plain kernel, its widths, groups of more than 8
+    ("fp32", 4, 2, 256, 16, [70, 33]), ("fp32", 10, 2, 6, 4, [9, 40]), ("fp32", 3, 1, 128, 16, [200, 1]), ("fp32", 1, 1, 64, 64, [300]),
+    ("bf16", 4, 2, 100, 16, [50, 129]), ("bf16", 9, 1, 36, 16, [64, 31]), ("bf16", 20, 2, 128, 32, [100, 65]), ("bf16", 2, 2, 16, 8, [33, 5]),
+    ("bf16", 16, 2, 64, 16, [2000, 31, 32, 33]), ("bf16", 5, 1, 256, 24, [900, 4])]
+
+
+@pytest.mark.parametrize("quant", [False, True])
+@pytest.mark.parametrize("dtype,H,Hkv,hd,page,lens", MORE)
+def test_attention_other_shapes(dtype, H, Hkv, hd, page, lens, quant):
+    cache = S.make_cache(R, len(lens), Hkv, hd, max(lens) + 1, page, dtype, quant, 30)
+    _poison(cache, lens, loop=0)
+    q = torch.randn(len(lens), H, hd, generator=torch.Generator().manual_seed(31)).to(DT[dtype]).cuda()
+    S.check_attention(cache, q, lens, R.paged_attention(q, _i32(lens), cache))
+    assert cache.read_status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("quant", [False, True])
+def test_attention_many_short_sequences(dtype, quant):
+    """More sequences than lengths fit on chip, empty ones and single tokens among them."""
+    B, H, Hkv, hd = 700, 6, 2, 64
+    lens = [(b * 37) % 41 for b in range(B)]
+    cache = S.make_cache(R, B, Hkv, hd, 48, 16, dtype, quant, 32)
+    q = torch.randn(B, H, hd, generator=torch.Generator().manual_seed(33)).to(DT[dtype]).cuda()
+    out = R.paged_attention(q, _i32(lens), cache)
+    S.check_attention(cache, q, lens, out)
+    fewer = R.paged_attention(q[:5].contiguous(), _i32(lens[:5]), cache, workspace=R.paged_attention_workspace(cache, H))
+    S.check_attention(cache, q[:5], lens[:5], fewer)
+
+
+@pytest.mark.parametrize("quant", [False, True])
+def test_bases_off_16_bytes(quant):
+    """Pools, rows and outputs whose addresses 16 does not divide take the value-wise paths."""
+    Hkv, hd, page, n = 2, 64, 16, 40
+    good = S.make_cache(R, 1, Hkv, hd, n, page, "bf16", quant, 34, fill=False)
+
+    def moved(t):
+        flat = torch.zeros(t.numel() + 8, dtype=torch.uint8 if quant else t.dtype, device="cuda")
+        view = flat[1:1 + t.numel()]
+        return (view.view(t.dtype) if quant else view).view(t.shape)
+    exps = [torch.zeros_like(good.k_exp) if quant else None for _ in range(2)]
+    odd = R.PagedKVCache(moved(good.k), moved(good.v), good.page_table, *exps, dtype="bf16")
+    g = torch.Generator().manual_seed(35)
+    rows = torch.randn(2, n, Hkv, hd, generator=g).to(torch.bfloat16).cuda()
+    q = torch.randn(1, 6, hd, generator=g).to(torch.bfloat16).cuda()
+    pos = torch.arange(n, dtype=torch.int32, device="cuda")
+    for c in (good, odd):
+        R.paged_kv_write(rows[0], rows[1], pos, c, seq=n)
+    for a, b in zip(R.paged_kv_read(_i32([n]), good, t_out=n), R.paged_kv_read(_i32([n]), odd, t_out=n)):
+        assert torch.equal(a, b)
+    S.check_attention(good, q, [n], R.paged_attention(q, _i32([n]), good))
+    S.check_attention(good, q, [n], R.paged_attention(q, _i32([n]), odd))
+    buf = torch.zeros(6 * hd + 1, dtype=torch.bfloat16, device="cuda")[1:].view(1, 6, hd)
+    R.paged_attention(q, _i32([n]), good, out=buf)
+    S.check_attention(good, q, [n], buf)
+
+
+def test_two_workspaces_on_two_streams():
+    """Two calls in flight together, each with its own workspace, give what each gives alone."""
+    cache = S.make_cache(R, 6, 2, 128, 700, 16, "bf16", False, 36)
+    g = torch.Generator().manual_seed(37)
+    qs = [torch.randn(6, 8, 128, generator=g).to(torch.bfloat16).cuda() for _ in range(2)]
+    lens = [_i32([700, 3, 0, 333, 64, 512]), _i32([1, 699, 200, 17, 0, 90])]
+    alone = [R.paged_attention(q, n, cache) for q, n in zip(qs, lens)]
+    ws = [R.paged_attention_workspace(cache, 8) for _ in range(2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        outs = []
+        for q, n, w, s in zip(qs, lens, ws, streams):
+            with torch.cuda.stream(s):
+                outs.append(R.paged_attention(q, n, cache, workspace=w))
+        torch.cuda.synchronize()
+        for a, b in zip(outs, alone):
+            assert torch.equal(a, b)

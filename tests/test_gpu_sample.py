@@ -14,6 +14,7 @@ pytestmark = pytest.mark.gpu
 
 R = pytest.importorskip("recurrent_depth_moe_b200")
 MARGIN = 4e-7
+ALL = 1 << 30
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -30,6 +31,9 @@ def _check(x, u, T, k, p, m, got, lp, max_near=0):
         tok, logp, margin = S.sample_row(x[i], float(u[i]), at(T), int(at(k)), at(p), at(m))
         if margin <= MARGIN:
             near += 1
+            if max_near == ALL:                       # the drawn token's share holds u, up to two borders' movement
+                lo, hi = S.sample_interval(x[i], int(got[i]), at(T), int(at(k)), at(p), at(m))
+                assert lo - 2 * MARGIN <= float(u[i]) <= hi + 2 * MARGIN, i
             continue
         assert int(got[i]) == tok, f"row {i}: token {int(got[i])}, the definition's is {tok} (margin {margin:.2e})"
         # a logarithm of a ratio of sums off by 2^-22, rounded to fp32
@@ -222,3 +226,59 @@ def test_large_vocabularies(V, n):
             eps = 2e-6                                               # the drawn token's interval holds u up to the sums' rounding
             assert float(by[t]) > 0 and lo - eps <= float(u[i]) < hi + eps, (i, lo, hi, float(u[i]))
             assert abs(float(lp[i]) - math.log(float(by[t]) / float(cum[-1]))) < 1e-5
+
+
+@pytest.mark.parametrize("kw", [dict(top_k=40), dict(top_k=20000), dict(top_k=59000), dict(top_p=0.9), dict(top_p=0.3), dict(top_p=0.9999),
+                                dict(top_k=40, top_p=0.8), dict(top_k=20000, top_p=0.7), dict(top_k=300, top_p=0.9, min_p=0.02)])
+def test_logits_of_few_distinct_values(kw):
+    """Logits rounded to bf16 (hundreds of tokens share a value, so a border falls among equal
+    logits and the lowest indices stay), with kept sets from tens of tokens to nearly all.  Far
+    out a token holds less of the weight than MARGIN (normal logits of deviation 2 have their
+    weight spread around 4 with that deviation, top_p 0.9999 ends 3.7 deviations below, at -3.4,
+    where a token holds exp(-3.4 - 2) / 60000 = 8e-8 of the total), so every row is near some
+    border there and is held to its token's share instead."""
+    V, n = 60000, 3
+    g = torch.Generator().manual_seed(51)
+    x = (torch.randn(n, V, generator=g) * 2.0).bfloat16().float()
+    u = torch.rand(n, generator=g)
+    tok, lp = R.sample_tokens(x.cuda(), u.cuda(), 1.0, return_logprob=True, **kw)
+    f32 = lambda a: float(torch.tensor(a, dtype=torch.float32))
+    _check(x, u, 1.0, kw.get("top_k", 0), f32(kw.get("top_p", 1.0)), f32(kw.get("min_p", 0.0)), tok.cpu(), lp.cpu(), max_near=ALL)
+
+
+@pytest.mark.parametrize("V", [4000, 60000, 201088, 500000])
+def test_rows_of_one_value(V):
+    """Every logit the same: top-k and top-p keep the first indices, and the draw is uniform over
+    them; also with one token above the rest, and with all weight in few equal tokens."""
+    u = torch.tensor([0.0, 0.3, 0.77, 1 - 2.0 ** -24])
+    x = torch.full((4, V), -1.5)
+    k = V // 3
+    tok = R.sample_tokens(x.cuda(), u.cuda(), 0.9, top_k=k)
+    assert tok.tolist() == [int(float(a) * k) for a in u]
+    tok = R.sample_tokens(x.cuda(), u.cuda(), 0.9, top_p=0.5)        # the first whose sum reaches half: ceil(V / 2) of them
+    assert tok.tolist() == [int(float(a) * ((V + 1) // 2)) for a in u]
+    x[:, V - 1] = 40.0
+    for kw in (dict(), dict(top_p=0.9), dict(top_k=5), dict(top_k=k, top_p=0.9)):
+        assert R.sample_tokens(x.cuda(), u.cuda(), 1.0, **kw).tolist()[1:] == [V - 1] * 3, kw
+    x[:, V // 2:V // 2 + 1500] = 40.0                                # 1501 equal tokens above all others
+    pos = list(range(V // 2, V // 2 + 1500)) + [V - 1]
+    assert R.sample_tokens(x.cuda(), u.cuda(), 1.0, top_k=1200).tolist() == [pos[int(float(a) * 1200)] for a in u]
+    kept = math.ceil(float(torch.tensor(0.5)) * 1501)
+    assert R.sample_tokens(x.cuda(), u.cuda(), 1.0, top_p=0.5, min_p=0.5).tolist() == [pos[int(float(a) * kept)] for a in u]
+
+
+def test_two_streams_at_once():
+    """Two calls in flight together, each as alone (no state is shared between calls)."""
+    x, u, g = _rows(40, 50257, 61)
+    y, v, _ = _rows(40, 50257, 62)
+    xc, uc, yc, vc = x.cuda(), u.cuda(), y.cuda(), v.cuda()
+    a, b = R.sample_tokens(xc, uc, 0.8, top_p=0.9), R.sample_tokens(yc, vc, 1.2, 64)
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(5):
+        with torch.cuda.stream(s1):
+            a2 = R.sample_tokens(xc, uc, 0.8, top_p=0.9)
+        with torch.cuda.stream(s2):
+            b2 = R.sample_tokens(yc, vc, 1.2, 64)
+        torch.cuda.synchronize()
+        assert torch.equal(a, a2) and torch.equal(b, b2)
