@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(32 * WARPS, HD <= 128 ? Tile<HD, Q>::CTAS : 1)
   auto slot_of = [&]() -> long long {
     const int key = it * KEYS + lane;
     if (left <= 0 || lane >= KEYS || key >= ilen) return -1;   // (lengths are within the table)
-    const int pi = p.ps_shift >= 0 ? key >> p.ps_shift : key / ps;
+    const int pi = page_index(p.c, key);
     const int page = __ldg(table + pi);
     if ((unsigned)page >= (unsigned)p.c.n_pages) {
       record_status(p.st, ST_BOUNDS, 222, page);
@@ -728,7 +728,7 @@ __global__ void __launch_bounds__(128) k_paged_attn_simt(PagedAttnParams p, int 
         long long s = -1;
         if (key < len) {
           const int page = page_of(p.c, b, key, p.st, 222);
-          if (page >= 0) s = ((long long)page * Hkv + g) * p.c.page_size + key % p.c.page_size;
+          if (page >= 0) s = ((long long)page * Hkv + g) * p.c.page_size + (key - page_index(p.c, key) * p.c.page_size);
         }
         slot_s[(t & (BUF - 1)) * TK + tid] = s;
       }
@@ -1014,9 +1014,6 @@ size_t paged_attn_scratch(const PagedView& c) {
 int launch_paged_attn(int dtype, const PagedAttnParams& p0, cudaStream_t s) {
   PagedAttnParams p = p0;
   const bool tc = mma_takes(dtype, p.c);
-  p.ps_shift = -1;
-  for (int i = 0; i < 31; ++i)
-    if (p.c.page_size == 1 << i) p.ps_shift = i;
   const int eb = p.c.e4m3 ? 1 : dtype == 0 ? 4 : 2, G = p.H / p.c.Hkv;
   const bool vec = p.c.hd % 4 == 0 && !(((uintptr_t)p.c.k | (uintptr_t)p.c.v) & (4 * eb - 1));
   const int nh = G >= 5 ? 8 : G >= 3 ? 4 : G, buffers = vec && dtype == 0 && !p.c.e4m3 ? 2 : 1;

@@ -41,6 +41,7 @@ template <typename T> __device__ __forceinline__ uint4 pack(const float (&x)[Vec
   return make_uint4(u[0], u[1], u[2], u[3]);
 }
 constexpr int NT = 128;
+__device__ __forceinline__ int slot_of(const PagedView& c, int pos) { return pos - page_index(c, pos) * c.page_size; }
 }  // namespace
 
 // One warp per (row, kv head): K, then V, value by value.
@@ -52,9 +53,9 @@ __global__ void __launch_bounds__(NT) k_paged_write(PagedWriteParams p) {
   const int row = (int)(wid / Hkv), g = (int)(wid % Hkv);
   const int pos = p.pos[row];
   if (pos < 0) return;
-  const int page = page_of(p.c, row / p.seq, pos, p.st, 201);
+  const int page = page_of(p.c, p.seq == 1 ? row : row / p.seq, pos, p.st, 201);
   if (page < 0) return;
-  const long long slot = ((long long)page * Hkv + g) * p.c.page_size + pos % p.c.page_size;
+  const long long slot = ((long long)page * Hkv + g) * p.c.page_size + slot_of(p.c, pos);
 #pragma unroll
   for (int kv = 0; kv < 2; ++kv) {
     const T* src = (const T*)(kv ? p.v : p.k) + (long long)row * p.ld + (long long)g * hd;
@@ -79,9 +80,9 @@ template <typename T, bool Q, int GL>
 __global__ void __launch_bounds__(NT) k_paged_write_vec(PagedWriteParams p) {
   constexpr int N = Vec<T>::N, RPT = GL == 32 && sizeof(T) == 4 ? 2 : 1;   // pieces of a lane
   const int gl = threadIdx.x % GL, Hkv = p.c.Hkv, hd = p.c.hd;
-  const long long id = ((long long)blockIdx.x * NT + threadIdx.x) / GL;
-  if (id >= (long long)p.n_rows * Hkv) return;             // (whole groups leave: shuffles stay inside one)
-  const int row = (int)(id / Hkv), g = (int)(id % Hkv);
+  const unsigned id = blockIdx.x * (unsigned)(NT / GL) + threadIdx.x / GL;   // (rows x heads fit 31 bits)
+  if (id >= (unsigned)p.n_rows * (unsigned)Hkv) return;    // (whole groups leave: shuffles stay inside one)
+  const int row = (int)(id / (unsigned)Hkv), g = (int)(id - (unsigned)row * (unsigned)Hkv);
   const int pos = __ldg(p.pos + row);
   if (pos < 0) return;
   const long long src = (long long)row * p.ld + (long long)g * hd;
@@ -92,9 +93,9 @@ __global__ void __launch_bounds__(NT) k_paged_write_vec(PagedWriteParams p) {
     w[0][i] = d < hd ? __ldcs(reinterpret_cast<const uint4*>((const T*)p.k + src + d)) : make_uint4(0, 0, 0, 0);
     w[1][i] = d < hd ? __ldcs(reinterpret_cast<const uint4*>((const T*)p.v + src + d)) : make_uint4(0, 0, 0, 0);
   }
-  const int page = page_of(p.c, row / p.seq, pos, p.st, 201);
+  const int page = page_of(p.c, p.seq == 1 ? row : row / p.seq, pos, p.st, 201);
   if (page < 0) return;
-  const long long slot = ((long long)page * Hkv + g) * p.c.page_size + pos % p.c.page_size;
+  const long long slot = ((long long)page * Hkv + g) * p.c.page_size + slot_of(p.c, pos);
   const unsigned group = GL == 32 ? 0xffffffffu : ((1u << GL) - 1) << ((threadIdx.x & 31) / GL * GL);
 #pragma unroll
   for (int kv = 0; kv < 2; ++kv) {
@@ -154,7 +155,7 @@ __global__ void __launch_bounds__(NT) k_paged_read(PagedReadParams p) {
   if (t >= n) return;
   const int page = page_of(p.c, b, t, p.st, 212);
   if (page < 0) return;
-  const long long slot = ((long long)page * Hkv + g) * p.c.page_size + t % p.c.page_size;
+  const long long slot = ((long long)page * Hkv + g) * p.c.page_size + slot_of(p.c, t);
   const long long out = (((long long)b * Hkv + g) * p.t_out + t) * hd;
 #pragma unroll
   for (int kv = 0; kv < 2; ++kv) {
@@ -186,7 +187,7 @@ __global__ void __launch_bounds__(NT) k_paged_read_vec(PagedReadParams p, int rt
     long long s = -1;
     if (t < n) {
       const int page = page_of(p.c, b, t, p.st, 212);
-      if (page >= 0) s = ((long long)page * Hkv + g) * p.c.page_size + t % p.c.page_size;
+      if (page >= 0) s = ((long long)page * Hkv + g) * p.c.page_size + slot_of(p.c, t);
     }
     slot_s[tid] = s;
     if (Q && s >= 0) sc[0][tid] = exp_byte_scale(__ldg(p.c.ke + s)), sc[1][tid] = exp_byte_scale(__ldg(p.c.ve + s));

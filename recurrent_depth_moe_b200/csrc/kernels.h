@@ -258,6 +258,7 @@ struct PagedView {
   uint8_t* ke; uint8_t* ve;      // e4m3: exponent bytes [n_pages][Hkv][page_size]
   const int* table;
   int e4m3, n_pages, page_size, Hkv, hd, max_pages;
+  int ps_shift;                  // page_size is 1 << ps_shift, or -1
 };
 struct PagedWriteParams {
   PagedView c;
@@ -282,7 +283,6 @@ struct PagedAttnParams {
   float scale;
   void* scratch;                                // paged_attn_scratch() bytes
   float* part_o; float* part_ml;
-  int ps_shift;                                 // page_size is 1 << ps_shift, or -1
   DevStatus* st;
 };
 void launch_paged_write(int dtype, const PagedWriteParams& p, cudaStream_t s);

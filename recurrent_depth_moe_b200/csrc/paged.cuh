@@ -21,12 +21,10 @@ __device__ __forceinline__ float exp_byte_scale(int b) { return __int_as_float(b
 // exponent E of a row whose largest finite magnitude is amax: amax = m 2^x, 0.5 <= m < 1, and
 // 448 = 0.875 * 2^9
 __device__ __forceinline__ int row_exponent(float amax) {
-  if (!(amax > 0.f)) return -127;
-  int x;
-  const float m = frexpf(amax, &x);
-  return min(max(x - 9 + (m > 0.875f ? 1 : 0), -127), 127);
+  const int b = __float_as_int(amax);                            // x = (b >> 23) - 126; 0.875 is mantissa 0x600000
+  return max((b >> 23) - 126 - 9 + ((b & 0x7fffff) > 0x600000), -127);   // (subnormal rows, and 0: -127; at most 120)
 }
-__device__ __forceinline__ float pow2_neg(int E) { return __int_as_float(E == 127 ? 0x00400000 : (127 - E) << 23); }   // 2^-E
+__device__ __forceinline__ float pow2_neg(int E) { return __int_as_float((127 - E) << 23); }   // 2^-E, -127 <= E <= 120
 
 // magnitude for the row maximum: infinities and NaN take no part in the scale
 __device__ __forceinline__ float finite_abs(float x) {
@@ -50,10 +48,14 @@ __device__ __forceinline__ float e4m3_f(uint8_t q) {
   return __half2float(__half(__nv_cvt_fp8_to_halfraw(q, __NV_E4M3)));
 }
 
+// Which page of its sequence a position is in.
+__device__ __forceinline__ int page_index(const PagedView& c, int pos) {
+  return c.ps_shift >= 0 ? pos >> c.ps_shift : pos / c.page_size;
+}
 // Page of position pos of sequence b, or -1 (recorded in the status word) if the position or
 // the table's entry is out of range.
 __device__ __forceinline__ int page_of(const PagedView& c, int b, int pos, DevStatus* st, int where) {
-  const int pi = pos / c.page_size;
+  const int pi = page_index(c, pos);
   if (pos < 0 || pi >= c.max_pages) {
     record_status(st, ST_BOUNDS, where, pos);
     return -1;
