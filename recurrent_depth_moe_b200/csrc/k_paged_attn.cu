@@ -21,7 +21,14 @@
 // or 22 (fp16) bits at no cost.  e4m3 values become fp16, exactly; a row's exponent of K scales
 // its score, of V its weight, relative to the largest exponent so far.
 //
-// k_paged_attn_simt (fp32 model, other widths): a lane per key and per channel in fp32.
+//
+// Measured on one B200 (128 channels; share of the measured copy rate, 6548.5 GB/s): one sequence
+// of 131,071 keys, 32 heads on 8, bf16 98 us (84%); 64 sequences of 1 to 4224 keys, 24 heads on 8,
+// bf16 106 us (80%), bound by HBM with a quarter of the issue slots used; 128 sequences of 4097 to
+// 8191 keys in e4m3 326 us (76%), bound by issue (48% active with 12 warps on an SM).
+//
+// k_paged_attn_simt (fp32 model, other widths): a lane per key and per channel in fp32; 64
+// sequences of 1000 to 2000 keys in fp32 172 us (70%).
 #include "paged.cuh"
 
 #include <algorithm>

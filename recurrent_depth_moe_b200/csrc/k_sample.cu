@@ -22,6 +22,12 @@
 // bin) brackets the border of top-k or top-p, the few tokens of the bracket become candidates,
 // and histograms over their (logit, index) order narrow the border to at most 32 of them, which
 // one warp ranks.  The kept tokens are then those at or before one (logit, index) pair.
+//
+// Measured on one B200, us: a row of 201,088 logits with top-p 29; 64 such rows with mixed
+// parameters 69; 256 with top-p 312 (the logits at the copy rate: 31).  Each row passes up to seven
+// cluster barriers, each about 2 us with the remote reads behind it, and that chain bounds it: of
+// 44 us that a wave of 37 clusters takes, 7 are the load, 15 the passes and 20 the barriers and
+// exchanges.
 #include "common.cuh"
 #include "kernels.h"
 
@@ -395,8 +401,11 @@ template <bool RES, int NT> struct Sampler {
   // The bin of refinement `par` in which the running measure (number, or with MASS weight; `base`
   // before the first bin) reaches `want`, into sh.ib[0], with the measure before it and the number
   // of candidates in it in sh.bc.  False: it is not reached.
-  template <bool MASS> __device__ __forceinline__ bool reach(int par, u64 base, u64 want) {
-    u64 c[2] = {0, 0}, m[2] = {0, 0};
+  struct Level {
+    u64 c[2], m[2];   // bins 2 * thread, + 1
+  };
+  template <bool MASS> __device__ __forceinline__ Level level_sums(int par) {
+    Level v = {{0, 0}, {0, 0}};
     if (threadIdx.x < RB / 2) {
       uint2 hc[CMAX];
       ulonglong2 hm[CMAX];
@@ -407,20 +416,23 @@ template <bool RES, int NT> struct Sampler {
                               : make_ulonglong2(0, 0);
       }
 #pragma unroll
-      for (int r = 0; r < CMAX; ++r) c[0] += hc[r].x, c[1] += hc[r].y, m[0] += hm[r].x, m[1] += hm[r].y;
+      for (int r = 0; r < CMAX; ++r) v.c[0] += hc[r].x, v.c[1] += hc[r].y, v.m[0] += hm[r].x, v.m[1] += hm[r].y;
     }
-    if (!MASS) m[0] = c[0], m[1] = c[1];
+    if (!MASS) v.m[0] = v.c[0], v.m[1] = v.c[1];
+    return v;
+  }
+  __device__ __forceinline__ bool reach(const Level& v, u64 base, u64 want) {
     u64 total;
-    u64 at = base + block_scan<NW>(m[0] + m[1], sh.red, total) - (m[0] + m[1]);
+    u64 at = base + block_scan<NW>(v.m[0] + v.m[1], sh.red, total) - (v.m[0] + v.m[1]);
     if (base + total < want) return false;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      if (at < want && want <= at + m[i]) {
+      if (at < want && want <= at + v.m[i]) {
         sh.ib[0] = 2 * threadIdx.x + i;
         sh.bc[0] = at;
-        sh.bc[1] = c[i];
+        sh.bc[1] = v.c[i];
       }
-      at += m[i];
+      at += v.m[i];
     }
     __syncthreads();
     return true;
@@ -488,7 +500,7 @@ template <bool RES, int NT> struct Sampler {
         if (MASS) atomicAdd(&sh.mass[par][b], wt(x));
       });
       cluster_sync(cl, C);
-      if (!reach<MASS>(par, base, want)) return false;
+      if (!reach(level_sums<MASS>(par), base, want)) return false;
       const u64 b = sh.ib[0];
       base = sh.bc[0];
       n = sh.bc[1];
@@ -500,17 +512,17 @@ template <bool RES, int NT> struct Sampler {
     }
     return rank_last<MASS>(ph, all, in, lo, hi, [](float) { return true; }, base, want, place);
   }
-  // The same for the candidates that list_each4 has counted in refinement `par` (a cluster
-  // barrier after it): with at most 32 in the bin that reaches `want` they are ranked at once,
+  // The same for the candidates that list_each4 has counted in a refinement, whose sums are v (taken
+  // after a cluster barrier): with at most 32 in the bin that reaches `want` they are ranked at once,
   // else (many equal logits, a list that is full) narrowed by their places.
   template <bool MASS>
-  __device__ bool settle(int ph, int par, const Steps& steps, const Cut& in, u64 base, u64 want, u64& place) {
+  __device__ bool settle(int ph, const Level& v, const Steps& steps, const Cut& in, u64 base, u64 want, u64& place) {
     u64 n, lo, hi;
     bool all;
     range(ph, n, lo, hi, all);
     if (n == 0) return false;
     if (!all) {
-      if (!reach<MASS>(par, base, want)) return false;
+      if (!reach(v, base, want)) return false;
       const int bin = sh.ib[0];
       const u64 before = sh.bc[0], here = sh.bc[1];
       __syncthreads();
@@ -674,7 +686,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_sample(SampleParams p, int ch
     }
     if (border) {
       const Cut in{bhi, 0};                                      // (the places leave only the candidates)
-      listed = sm.template settle<false>(0, par, Steps(blo, bhi), in, before, (u64)k, cut.place) && blo == MAGIC && !all;
+      listed = sm.template settle<false>(0, sm.template level_sums<false>(par), Steps(blo, bhi), in, before, (u64)k, cut.place) && blo == MAGIC && !all;
       listed_steps = Steps(blo, bhi);
       cut.L = wt.bin(of_key((uint32_t)(cut.place >> IDX_BITS)));
     }
@@ -707,9 +719,10 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_sample(SampleParams p, int ch
       if (lane == 0) sh.total = total;
     }
     cluster_sync(cl, C);
+    const auto level = sm.template level_sums<true>(par);
     total = warp_sum64(lane < C ? *cl.map_shared_rank(&sh.total, lane) : 0);
     const u64 want = (u64)max(1.0, ceil((double)fmaxf(top_p, 0.f) * (double)total));
-    sm.template reach<true>(par, 0, want);                       // (the total is the bins' own)
+    sm.reach(level, 0, want);                       // (the total is the bins' own)
     const int bin = sh.ib[0];
     const u64 before = sh.bc[0], here = sh.bc[1];
     __syncthreads();
@@ -812,13 +825,14 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_sample(SampleParams p, int ch
       if (lane == 0) sh.total = t, sh.above = a;
     }
     cluster_sync(cl, C);
+    const auto level = sm.template level_sums<true>(par);        // (with the other remote reads)
     total = warp_sum64(lane < C ? *cl.map_shared_rank(&sh.total, lane) : 0);
     above = warp_sum64(lane < C ? *cl.map_shared_rank(&sh.above, lane) : 0);
     const u64 want = (u64)max(1.0, ceil((double)fmaxf(top_p, 0.f) * (double)total));
     u64 place = 0;
     const bool full = __any_sync(0xffffffffu, lane < C && *cl.map_shared_rank(&sh.fcnt[1], min(lane, C - 1)) > LCAP);
     summed = above < want && !full;
-    const bool ok = above < want && sm.template settle<true>(1, par, steps, cut, above, want, place);
+    const bool ok = above < want && sm.template settle<true>(1, level, steps, cut, above, want, place);
     if (!ok) {                                                   // the bracket missed the border: the whole order
       cluster_sync(cl, C);
       if (tid == 0) sh.gcnt[1] = 0;
@@ -945,9 +959,11 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_sample(SampleParams p, int ch
 
 // Cluster size: two CTAs on an SM can hold 100 KB of a row each, so that one's passes run while
 // the other loads; with few rows the cluster grows, down to 4096 logits a CTA.
-// 512 threads: with 256 a CTA issues a sixth fewer instructions (what it does beside the passes
-// costs every warp the same) but waits longer for each: 432 us instead of 358 for 256 rows of
-// 201,088 logits with top-p.
+// Threads: with 256 a CTA issues fewer instructions (what it does beside the passes costs every
+// warp the same) but waits longer for each.  More short rows than SMs run better with them (512
+// rows of 8000 logits with top-p: 31 us, with 512 threads 43); others do not (33 rows of 4000
+// without it: 10.8 us, with 512 threads 8.7; 256 rows of 201,088 with it, in an earlier state:
+// 432 us, with 512 threads 358).
 int launch_sample(const SampleParams& p, cudaStream_t s) {
   const int quads = p.vocab / 4 + 2;                             // whatever the row's alignment
   const int sms = device_sm_count();
@@ -955,11 +971,12 @@ int launch_sample(const SampleParams& p, cudaStream_t s) {
   while (C < CMAX && ((quads + C - 1) / C > 25200 / 4 || ((long long)p.n * C < sms && quads > C * 2048))) C *= 2;
   const int chunk = (quads + C - 1) / C, most = 227 * 1024 - 1024 - (int)sizeof(Shared);
   const bool res = (long long)chunk * 16 <= most;
-  void (*kernel)(SampleParams, int) = res ? k_sample<true, 512> : k_sample<false, 512>;
+  const bool small = p.vocab <= 8192 && p.n > sms;
+  void (*kernel)(SampleParams, int) = small ? k_sample<true, 256> : res ? k_sample<true, 512> : k_sample<false, 512>;
   if (!ensure_smem_limit((const void*)kernel, res ? most : 0)) return -1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(p.n * (long long)C));
-  cfg.blockDim = dim3(512);
+  cfg.blockDim = dim3(small ? 256 : 512);
   cfg.dynamicSmemBytes = res ? (size_t)chunk * 16 : 0;
   cfg.stream = s;
   cudaLaunchAttribute at[1];
