@@ -202,7 +202,8 @@ class RecurrentBlock:
                 act_threshold: float = 0.0, start_pos: int = 0, halt_logit_offset: Optional[torch.Tensor] = None,
                 cache: Union[KVCache, PagedKVCache, None] = None, trace: Optional[Trace] = None, flags: int = 0,
                 out: Optional[tuple] = None, workspace: Optional[torch.Tensor] = None):
-        """rdt_recurrent_forward (rdt_recurrent_forward_paged over a paged cache).  Returns (h_out [N, D] fp32, halt_weights [L, N] fp32,
+        """rdt_recurrent_forward (rdt_recurrent_forward_paged over a paged cache).  Returns
+        (h_out [N, D] fp32, halt_weights [L, N] fp32,
         expert_ids [L, N, k] int32)."""
         lib = N.load()
         cfg = self.cfg
@@ -306,8 +307,9 @@ class DecodeGraph:
     replays it, every later call replays.  Calls made while the library's profiler records
     run eagerly, since its CUDA events are recorded at launch time."""
 
-    def __init__(self, blk: "RecurrentBlock", batch: int, cache: Union[KVCache, PagedKVCache], cache_len: torch.Tensor, n_loops: int,
-                 act_threshold: float = 0.0, workspace: Optional[torch.Tensor] = None, out: Optional[tuple] = None,
+    def __init__(self, blk: "RecurrentBlock", batch: int, cache: Union[KVCache, PagedKVCache],
+                 cache_len: torch.Tensor, n_loops: int, act_threshold: float = 0.0,
+                 workspace: Optional[torch.Tensor] = None, out: Optional[tuple] = None,
                  halt_logit_offset: bool = False):
         cfg = blk.cfg
         self.blk, self.B, self.cache, self.cache_len = blk, batch, cache, cache_len

@@ -57,7 +57,9 @@ constexpr int LENS = 512;           // lengths kept in shared memory (of a longe
 struct Lens {
   const PagedAttnParams& p;
   const int* kept;                  // shared memory, or null
-  __device__ __forceinline__ int keys(int b) const { return kept ? kept[b] : visible_keys(p.c, p.lens, b, p.len_add, nullptr, 0); }
+  __device__ __forceinline__ int keys(int b) const {
+    return kept ? kept[b] : visible_keys(p.c, p.lens, b, p.len_add, nullptr, 0);
+  }
   __device__ __forceinline__ int tiles(int b, int tile) const { return (keys(b) + tile - 1) / tile; }
   __device__ __forceinline__ int units(int b, int tile) const {
     const int n = tiles(b, tile);
@@ -488,31 +490,31 @@ __global__ void __launch_bounds__(32 * WARPS, HD <= 128 ? Tile<HD, Q>::CTAS : 1)
         for (int kk = 0; kk < NG; kk += 2)
 #pragma unroll
           for (int h = 0; h < VH; ++h) {
-            {
-              // (e4m3 rows of 64 have 4 pieces: the upper lanes' channels do not exist)
-              const int cc = PIECES % 8 ? (h * 8 + n8) % PIECES : h * 8 + n8, r = kk * 8 + 2 * j4;
-              const uint4 v0 = lds16(va + r * ROW + swz_v<PIECES>(r, cc) * 16), v1 = lds16(va + (r + 1) * ROW + swz_v<PIECES>(r + 1, cc) * 16);
-              const uint4 v2 = lds16(va + (r + 8) * ROW + swz_v<PIECES>(r + 8, cc) * 16), v3 = lds16(va + (r + 9) * ROW + swz_v<PIECES>(r + 9, cc) * 16);
-              const uint32_t x0[4] = {v0.x, v0.y, v0.z, v0.w}, x1[4] = {v1.x, v1.y, v1.z, v1.w};
-              const uint32_t x2[4] = {v2.x, v2.y, v2.z, v2.w}, x3[4] = {v3.x, v3.y, v3.z, v3.w};
-              if (!Q) {
+            // (e4m3 rows of 64 have 4 pieces: the upper lanes' channels do not exist)
+            const int cc = PIECES % 8 ? (h * 8 + n8) % PIECES : h * 8 + n8, r = kk * 8 + 2 * j4;
+            uint32_t x[4][4];                           // keys r, r + 1, r + 8, r + 9
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {           // channels 2 u, 2 u + 1 of the piece
-                  mma<Q>(acc[h * 8 + 2 * u], ph[kk], pl[kk], ph[kk + 1], pl[kk + 1], __byte_perm(x0[u], x1[u], 0x5410),
-                         __byte_perm(x2[u], x3[u], 0x5410));
-                  mma<Q>(acc[h * 8 + 2 * u + 1], ph[kk], pl[kk], ph[kk + 1], pl[kk + 1], __byte_perm(x0[u], x1[u], 0x7632),
-                         __byte_perm(x2[u], x3[u], 0x7632));
-                }
-              } else {
+            for (int i = 0; i < 4; ++i) {
+              const int ri = r + (i & 1) + 8 * (i >> 1);
+              const uint4 v = lds16(va + ri * ROW + swz_v<PIECES>(ri, cc) * 16);
+              x[i][0] = v.x, x[i][1] = v.y, x[i][2] = v.z, x[i][3] = v.w;
+            }
+            auto add = [&](float(&o)[4], uint32_t b0, uint32_t b1) {
+              mma<Q>(o, ph[kk], pl[kk], ph[kk + 1], pl[kk + 1], b0, b1);
+            };
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {           // channels 4 u .. 4 u + 3
-                  const uint32_t a0 = __byte_perm(x0[u], x1[u], 0x5140), a1 = __byte_perm(x0[u], x1[u], 0x7362);
-                  const uint32_t b0 = __byte_perm(x2[u], x3[u], 0x5140), b1 = __byte_perm(x2[u], x3[u], 0x7362);
-                  mma<Q>(acc[h * 16 + 4 * u], ph[kk], pl[kk], ph[kk + 1], pl[kk + 1], e4m3x2_h2(a0 & 0xffff), e4m3x2_h2(b0 & 0xffff));
-                  mma<Q>(acc[h * 16 + 4 * u + 1], ph[kk], pl[kk], ph[kk + 1], pl[kk + 1], e4m3x2_h2(a0 >> 16), e4m3x2_h2(b0 >> 16));
-                  mma<Q>(acc[h * 16 + 4 * u + 2], ph[kk], pl[kk], ph[kk + 1], pl[kk + 1], e4m3x2_h2(a1 & 0xffff), e4m3x2_h2(b1 & 0xffff));
-                  mma<Q>(acc[h * 16 + 4 * u + 3], ph[kk], pl[kk], ph[kk + 1], pl[kk + 1], e4m3x2_h2(a1 >> 16), e4m3x2_h2(b1 >> 16));
-                }
+            for (int u = 0; u < 4; ++u) {
+              if (!Q) {                                 // channels 2 u, 2 u + 1 of the piece
+                add(acc[h * 8 + 2 * u], __byte_perm(x[0][u], x[1][u], 0x5410), __byte_perm(x[2][u], x[3][u], 0x5410));
+                add(acc[h * 8 + 2 * u + 1], __byte_perm(x[0][u], x[1][u], 0x7632), __byte_perm(x[2][u], x[3][u], 0x7632));
+              } else {                                  // channels 4 u .. 4 u + 3
+                const uint32_t a0 = __byte_perm(x[0][u], x[1][u], 0x5140), a1 = __byte_perm(x[0][u], x[1][u], 0x7362);
+                const uint32_t b0 = __byte_perm(x[2][u], x[3][u], 0x5140), b1 = __byte_perm(x[2][u], x[3][u], 0x7362);
+                float(*o)[4] = acc + h * EPP + EPP / 4 * u;
+                add(o[0], e4m3x2_h2(a0 & 0xffff), e4m3x2_h2(b0 & 0xffff));
+                add(o[1], e4m3x2_h2(a0 >> 16), e4m3x2_h2(b0 >> 16));
+                add(o[2 % (EPP / 4)], e4m3x2_h2(a1 & 0xffff), e4m3x2_h2(b1 & 0xffff));
+                add(o[3 % (EPP / 4)], e4m3x2_h2(a1 >> 16), e4m3x2_h2(b1 >> 16));
               }
             }
           }
@@ -621,17 +623,21 @@ __global__ void __launch_bounds__(32 * WARPS, HD <= 128 ? Tile<HD, Q>::CTAS : 1)
 #pragma unroll
         for (int k = 0; k < 2 * WARPS; ++k) {
           const float wk = __shfl_sync(0xffffffffu, w, k);
-          if (parts >> k & 1) o.x = fmaf(wk, v[k].x, o.x), o.y = fmaf(wk, v[k].y, o.y), o.z = fmaf(wk, v[k].z, o.z), o.w = fmaf(wk, v[k].w, o.w);
+          if (!(parts >> k & 1)) continue;
+          o.x = fmaf(wk, v[k].x, o.x), o.y = fmaf(wk, v[k].y, o.y);
+          o.z = fmaf(wk, v[k].z, o.z), o.w = fmaf(wk, v[k].w, o.w);
         }
         if (ch >= hd) continue;
         if (begun && ended) {
           bf16* y = (bf16*)p.o + (long long)b * p.o_row + (long long)(g * G + h0 + h) * hd + ch;
-          y[0] = from_f<bf16>(o.x * inv), y[1] = from_f<bf16>(o.y * inv), y[2] = from_f<bf16>(o.z * inv), y[3] = from_f<bf16>(o.w * inv);
+          y[0] = from_f<bf16>(o.x * inv), y[1] = from_f<bf16>(o.y * inv);
+          y[2] = from_f<bf16>(o.z * inv), y[3] = from_f<bf16>(o.w * inv);
         } else {
           *reinterpret_cast<float4*>(part_o(p, blockIdx.x, begun) + h * hd + ch) = o;
         }
       }
-      if (lane == 0 && !(begun && ended)) *reinterpret_cast<float2*>(part_ml(p, blockIdx.x, begun) + h * 2) = make_float2(M, L);
+      if (lane == 0 && !(begun && ended))
+        *reinterpret_cast<float2*>(part_ml(p, blockIdx.x, begun) + h * 2) = make_float2(M, L);
     }
     i = j;
   }

@@ -440,7 +440,8 @@ template <bool RES, int NT> struct Sampler {
   // The last place that stays among at most 32 candidates, those of phase ph that `is` holds:
   // the one at which the running measure, `base` before them, reaches `want`.
   template <bool MASS, typename F>
-  __device__ __forceinline__ bool rank_last(int ph, bool all, const Cut& in, u64 lo, u64 hi, F is, u64 base, u64 want, u64& place) {
+  __device__ __forceinline__ bool rank_last(int ph, bool all, const Cut& in, u64 lo, u64 hi, F is, u64 base, u64 want,
+                                            u64& place) {
     candidates(ph, all, in, lo, hi, [&](float x, u64 pl) {
       if (!is(x)) return;
       const uint32_t i = atomicAdd(&sh.gcnt[ph], 1u);
@@ -527,7 +528,8 @@ template <bool RES, int NT> struct Sampler {
       const u64 before = sh.bc[0], here = sh.bc[1];
       __syncthreads();
       if (here <= 32)
-        return rank_last<MASS>(ph, false, in, lo, hi, [&](float x) { return steps(wt, x) == bin; }, before, want, place);
+        return rank_last<MASS>(ph, false, in, lo, hi, [&](float x) { return steps(wt, x) == bin; }, before, want,
+                               place);
     }
     return resolve<MASS>(ph, all, in, lo, hi, n, base, want, place);
   }
@@ -599,7 +601,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_sample(SampleParams p, int ch
       p.tokens[(long long)r * p.out_ld] = best == 0x7fffffff ? 0 : (int)best;
       if (p.logprob) p.logprob[r] = 0.f;
     }
-    cluster_sync(cl, C);                                                   // remote shared memory is read until here
+    cluster_sync(cl, C);                                         // remote shared memory is read until here
     return;
   }
   if (mx == INFINITY) {
@@ -686,8 +688,9 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_sample(SampleParams p, int ch
     }
     if (border) {
       const Cut in{bhi, 0};                                      // (the places leave only the candidates)
-      listed = sm.template settle<false>(0, sm.template level_sums<false>(par), Steps(blo, bhi), in, before, (u64)k, cut.place) && blo == MAGIC && !all;
       listed_steps = Steps(blo, bhi);
+      const auto level = sm.template level_sums<false>(par);
+      listed = sm.template settle<false>(0, level, listed_steps, in, before, (u64)k, cut.place) && blo == MAGIC && !all;
       cut.L = wt.bin(of_key((uint32_t)(cut.place >> IDX_BITS)));
     }
     if (top_p < 1.f && !listed) {
@@ -722,7 +725,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_sample(SampleParams p, int ch
     const auto level = sm.template level_sums<true>(par);
     total = warp_sum64(lane < C ? *cl.map_shared_rank(&sh.total, lane) : 0);
     const u64 want = (u64)max(1.0, ceil((double)fmaxf(top_p, 0.f) * (double)total));
-    sm.reach(level, 0, want);                       // (the total is the bins' own)
+    sm.reach(level, 0, want);                                    // (the total is the bins' own)
     const int bin = sh.ib[0];
     const u64 before = sh.bc[0], here = sh.bc[1];
     __syncthreads();
