@@ -28,7 +28,7 @@
 // 8191 keys in e4m3 326 us (76%), bound by issue (48% active with 12 warps on an SM).
 //
 // k_paged_attn_simt (fp32 model, other widths): a lane per key and per channel in fp32; 64
-// sequences of 1000 to 2000 keys in fp32 172 us (70%).
+// sequences of 1000 to 2000 keys, 24 heads on 8, in fp32 171 us (70%), in e4m3 281 us (11%).
 #include "paged.cuh"
 
 #include <algorithm>
@@ -682,7 +682,7 @@ template <int NH> __device__ __forceinline__ Heads<NH> heads_at(const float* p) 
 }  // namespace
 
 template <typename T, bool Q, int NH, bool VEC>
-__global__ void __launch_bounds__(128, 4) k_paged_attn_simt(PagedAttnParams p, int least) {
+__global__ void __launch_bounds__(128, 5) k_paged_attn_simt(PagedAttnParams p, int least) {
   constexpr bool AHEAD = VEC && !Q && sizeof(T) == 4;   // copied as it is, a tile ahead
   constexpr int BUF = AHEAD ? 2 : 1, HW = (NH + WARPS - 1) / WARPS;   // heads of a warp
   extern __shared__ __align__(128) unsigned char smem[];
@@ -994,7 +994,7 @@ bool mma_takes(int dtype, const PagedView& c) {
   return dtype == 1 && c.hd % 8 == 0 && rb % 16 == 0 && !(((uintptr_t)c.k | (uintptr_t)c.v) & 15);
 }
 int ctas_mma(bool e4m3) { return device_sm_count() * (e4m3 ? Tile<128, true>::CTAS : Tile<128, false>::CTAS); }
-constexpr int SIMT_CTAS = 4;   // on an SM at most: registers (an fp32 tile of 128 channels, twice, is 68 KB: 3)
+constexpr int SIMT_CTAS = 5;   // on an SM at most (an fp32 tile of 128 channels, twice, is 68 KB: three)
 int ctas_simt(int smem) { return device_sm_count() * std::max(1, std::min(SIMT_CTAS, 227 * 1024 / (smem + 4096))); }
 // descriptors, then the parts of `ctas` CTAs and, on tensor cores, of their warps
 size_t scratch_bytes(int ctas, int parts, int hd) {
