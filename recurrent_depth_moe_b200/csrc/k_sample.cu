@@ -42,7 +42,7 @@ namespace rdt {
 
 namespace {
 constexpr int NWMAX = 16;        // warps of a CTA
-constexpr int BINS = 46 * 16;    // of the exponent: below 2^-46 a weight rounds to nothing
+constexpr int BINS = 46 * 16;    // of the exponent: a weight below 2^-45 is nothing
 constexpr int RB = 256;          // bins of one refinement
 constexpr int HB = BINS / 4;     // threads that sum the cluster's histograms, four bins each
 constexpr int LCAP = 1000;       // candidates one CTA lists (below 2^10: sums of their weights' halves stay in 32
@@ -91,7 +91,7 @@ __device__ __forceinline__ F2 operator-(F2 a, F2 b) { return fma2(b, F2(-1.f), a
 struct Weigh {
   float m, chi, clo, nfM, c16;   // log2(e) / T in two words; minus M's fraction; bins per logit
   float magic;                   // MAGIC minus M's whole part
-  float floor;                   // at and below it a weight rounds to nothing
+  float floor;                   // the smallest logit with a weight: 2^-45 of the maximum's
   bool wide;                     // |M| so large that z has no fraction left: the difference m - x is formed first
   static constexpr float MAGIC = 12582912.f;   // 1.5 * 2^23: x + MAGIC rounds x to a whole number
   __device__ Weigh(float mx, float T) : m(mx) {
@@ -104,11 +104,11 @@ struct Weigh {
     const float i0 = (Mh + MAGIC) - MAGIC;
     magic = MAGIC - i0;
     nfM = -((Mh - i0) + (fmaf(mx, chi, -Mh) + mx * clo));
-    floor = __double2float_rd((double)mx - 32.06 * (double)T);       // 46.25 / log2(e)
+    floor = __double2float_ru((double)mx - 31.191623125218536 * (double)T);   // 45 / log2(e)
   }
   // MAGIC plus the bin, 16 times the exponent rounded to a whole number; monotone in x, NaN for NaN
   __device__ __forceinline__ float bin(float x) const { return fmaf(m - x, c16, MAGIC); }
-  // the weight, to 24 bits (2^-46 for what is below floor, NaN too)
+  // the weight, to 24 bits (that of floor for what is below it, NaN too)
   template <bool WIDE> __device__ __forceinline__ float weight(float x) const {
     float s, e;
     int k;                                                           // minus the whole part of the exponent
@@ -147,10 +147,11 @@ struct Weigh {
     f = fma2(d, c, F2(MAGIC) - b);
     b.get(b0, b1);
   }
-  // in whole units of 2^-44
+  // In whole units of 2^-44, one at least from floor on: wherever sums of weights say that there is
+  // something, a token with a weight is found (the sums cut at floor too, by the same comparison).
   __device__ __forceinline__ u64 operator()(float x) const {
     const float w = wide ? weight<true>(x) : weight<false>(x);
-    return w >= 0x1p-45f && bin(x) < MAGIC + BINS ? __float2ull_rn(w * 0x1p44f) : 0;
+    return x >= floor ? max(1ull, __float2ull_rn(w * 0x1p44f)) : 0;
   }
 };
 
@@ -807,8 +808,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_sample(SampleParams p, int ch
         for (int e = 0; e < 4; e += 2) {
           float w0, w1;
           wt.template weight2<decltype(wide)::value>(x[e], x[e + 1]).get(w0, w1);
-          w0 = b[e] < MAGIC + BINS ? w0 : 0.f;
-          w1 = b[e + 1] < MAGIC + BINS ? w1 : 0.f;
+          w0 = x[e] >= wt.floor && !(decltype(with_cut)::value && b[e] == MAGIC + BINS) ? w0 : 0.f;
+          w1 = x[e + 1] >= wt.floor && !(decltype(with_cut)::value && b[e + 1] == MAGIC + BINS) ? w1 : 0.f;
           sum_total.add(F2(w0, w1));
           sum_above.add(F2(b[e] < blo ? w0 : 0.f, b[e + 1] < blo ? w1 : 0.f));
         }
