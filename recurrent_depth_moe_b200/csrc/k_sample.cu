@@ -7,7 +7,8 @@
 //   min-p: of these, those with w_v >= min_p.
 // The first of the order always stays.  The token drawn is the first v, in the vocabulary's
 // order, at which the running sum of the kept weights exceeds u times their total.
-// NaN logits take no part.  T <= 0, or a row with no weight: the most likely token.
+// NaN logits take no part.  T <= 0, or a row with no weight: the most likely token; an infinite T:
+// every logit above -inf weighs 1.
 //
 // The exponent (x - m) log2(e) / T is formed in two fp32 words, so a weight is off by about one
 // rounding of its 24 bits wherever it lies.  A thread sums its weights in two fp32 words, in a
@@ -32,6 +33,8 @@
 #include "kernels.h"
 
 #include <cooperative_groups.h>
+
+#include <float.h>
 
 #include <algorithm>
 #include <type_traits>
@@ -104,7 +107,9 @@ struct Weigh {
     const float i0 = (Mh + MAGIC) - MAGIC;
     magic = MAGIC - i0;
     nfM = -((Mh - i0) + (fmaf(mx, chi, -Mh) + mx * clo));
-    floor = __double2float_ru((double)mx - 31.191623125218536 * (double)T);   // 45 / log2(e)
+    // 45 / log2(e); finite, so that -inf has no weight, and within fp32's range of the maximum, so
+    // that m - x is finite from floor on (either only matters for T above 10^37)
+    floor = fmaxf(__double2float_ru((double)mx - 31.191623125218536 * (double)T), fmaxf(-FLT_MAX, mx - FLT_MAX));
   }
   // MAGIC plus the bin, 16 times the exponent rounded to a whole number; monotone in x, NaN for NaN
   __device__ __forceinline__ float bin(float x) const { return fmaf(m - x, c16, MAGIC); }
@@ -851,7 +856,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_sample(SampleParams p, int ch
   // min-p: (x - m) / T >= ln(min_p)
   float xmin = -INFINITY;
   if (min_p > 0.f) {
-    xmin = fminf(mx, __double2float_ru((double)mx + (double)T * log((double)fminf(min_p, 1.f))));
+    // (an infinite temperature: every weight is 1)
+    xmin = isinf(T) ? -INFINITY : fminf(mx, __double2float_ru((double)mx + (double)T * log((double)fminf(min_p, 1.f))));
   }
   const bool by_place = cut.place != 0;
   const float xcut = by_place ? of_key((uint32_t)(cut.place >> IDX_BITS)) : -INFINITY;

@@ -56,3 +56,54 @@ def test_background_at_the_smallest_weight(V, kw):
             assert int(tok[i]) in want, (gap, u, int(tok[i]))
             if int(tok[i]) == V - 1:
                 assert abs(float(lp[i])) <= 2.0 ** -20, (gap, u)
+
+
+@pytest.mark.parametrize("V", [500, 9001, 201088])
+def test_infinite_and_huge_temperatures_with_masked_logits(V):
+    """An infinite temperature is uniform over the tokens above -inf (NaN and -inf take no part),
+    and so is a finite one far above the logits, with every other parameter beside it."""
+    g = torch.Generator().manual_seed(V)
+    us = torch.tensor([0.0, 0.2, 0.55, 0.999, 1 - 2.0 ** -24])
+    x = torch.randn(len(us), V, generator=g) * 3
+    x[torch.rand(x.shape, generator=g) < 0.3] = -math.inf
+    x[:, 1::97] = math.nan
+    x[:, 7] = 0.5
+    for T in (math.inf, 3.4e38, 1e38, 1.1e37):
+        for kw in (dict(), dict(top_k=V - 2), dict(top_k=37), dict(min_p=0.5), dict(top_p=0.5), dict(top_k=V * 2, top_p=1.0)) + \
+                ((dict(min_p=1.0),) if T == math.inf else ()):
+            tok, lp = _sample(x, us, torch.full((len(us),), T), **kw)
+            for i in range(len(us)):
+                live = torch.nonzero(x[i] > -math.inf).flatten()
+                n = min(len(live), kw.get("top_k", V), math.ceil(kw.get("top_p", 1.0) * len(live)))
+                order = torch.sort(x[i, live], descending=True, stable=True).indices[:n]
+                live = live[order].sort().values                  # what is kept, in the vocabulary's order
+                pos = int(torch.searchsorted(live, int(tok[i])))
+                assert pos < n and int(live[pos]) == int(tok[i]), (T, kw, i, int(tok[i]))
+                # n equal weights: u n lies in the drawn token's unit, or within fp32's share of its ends
+                assert pos - n * 2.0 ** -21 <= float(us[i]) * n <= pos + 1 + n * 2.0 ** -21, (T, kw, i, pos)
+                assert abs(float(lp[i]) + math.log(n)) <= 2.0 ** -20 * math.log(n), (T, kw, i)
+
+
+def test_rows_of_the_lowest_value_and_minus_infinity():
+    """A row whose unmasked logits are all the type's lowest value, beside -inf."""
+    V = 3000
+    us = torch.tensor([0.0, 0.4, 0.9, 1 - 2.0 ** -24])
+    x = torch.full((4, V), -math.inf)
+    x[:, ::3] = LOWEST
+    n = 1000
+    for T in (1.0, 1e-3, 1e30):
+        for kw in (dict(), dict(top_k=2999), dict(min_p=0.9), dict(top_k=500), dict(top_p=0.5)):
+            tok, lp = _sample(x, us, T, **kw)
+            m = kw.get("top_k", n) if kw.get("top_k", n) < n else 500 if "top_p" in kw else n
+            for i in range(4):
+                assert int(tok[i]) == 3 * int(float(us[i]) * m), (T, kw, i)
+                assert abs(float(lp[i]) + math.log(m)) <= 2.0 ** -19, (T, kw, i)
+    y = torch.full((4, 200), LOWEST)                              # masked by the lowest value under a huge temperature
+    y[:, 100:] = torch.linspace(-1, 1, 100)
+    for T in (1e37, 1e38):
+        tok, lp = _sample(y, us, T)
+        t32 = float(torch.tensor(T))
+        for i in range(4):
+            want, logp, margin = S.sample_row(y[i], float(us[i]), t32)
+            assert int(tok[i]) == want or margin < 4e-7, (T, i)
+            assert margin < 4e-7 or abs(float(lp[i]) - logp) <= 2.0 ** -19, (T, i)
