@@ -736,12 +736,11 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_sample(SampleParams p, int ch
     const u64 before = sh.bc[0], here = sh.bc[1];
     __syncthreads();
     u64 place = 0;
-    if (here <= 32)
-      sm.template rank_last<true>(1, false, cut, cut.place, top, [&](float x) { return listed_steps(wt, x) == bin; }, before,
-                                  want, place);
-    else
-      sm.template resolve<true>(1, false, cut, cut.place, top, (u64)p.vocab, 0, want, place);
-    cut.place = place;
+    const bool ok = here <= 32 ? sm.template rank_last<true>(1, false, cut, cut.place, top,
+                                                             [&](float x) { return listed_steps(wt, x) == bin; }, before,
+                                                             want, place)
+                               : sm.template resolve<true>(1, false, cut, cut.place, top, (u64)p.vocab, 0, want, place);
+    if (ok) cut.place = place;
   } else if (top_p < 1.f) {
     // A weight is counted as 11 bits of 2^-(bin / 16) (2^20 of them fit 32 bits), interpolated
     // linearly in the bin (up to half a bin to each side): off by less than 5e-4 of it, so bins
@@ -841,17 +840,22 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_sample(SampleParams p, int ch
     u64 place = 0;
     const bool full = __any_sync(0xffffffffu, lane < C && *cl.map_shared_rank(&sh.fcnt[1], min(lane, C - 1)) > LCAP);
     summed = above < want && !full;
-    const bool ok = above < want && sm.template settle<true>(1, level, steps, cut, above, want, place);
-    if (!ok) {                                                   // the bracket missed the border: the whole order
+    bool ok = above < want && sm.template settle<true>(1, level, steps, cut, above, want, place);
+    // The bracket missed the border, as where 16 bins per power of two pass fp32's range (T below
+    // 7.7e-38): the whole order of what weighs something.
+    if (!ok) {
       cluster_sync(cl, C);
       if (tid == 0) sh.gcnt[1] = 0;
       if (tid < 32) sh.glist[1][tid] = 0;
       summed = false;
       __syncthreads();
-      sm.template resolve<true>(1, true, cut, 0, (1ull << (32 + IDX_BITS)) - 1, (u64)p.vocab, 0, want, place);
+      ok = sm.template resolve<true>(1, true, cut, (u64)key_of(wt.floor) << IDX_BITS, (1ull << (32 + IDX_BITS)) - 1,
+                                     (u64)p.vocab, 0, want, place);
     }
     cut.L = -1.f;                                                // the place alone decides
-    cut.place = place;
+    // (not reached: the weights rounded one by one sum to less than top_p of their sum, which then is
+    // within a rounding of 1, and top-k's border stays)
+    if (ok) cut.place = place;
   }
   // min-p: (x - m) / T >= ln(min_p)
   float xmin = -INFINITY;

@@ -107,3 +107,46 @@ def test_rows_of_the_lowest_value_and_minus_infinity():
             want, logp, margin = S.sample_row(y[i], float(us[i]), t32)
             assert int(tok[i]) == want or margin < 4e-7, (T, i)
             assert margin < 4e-7 or abs(float(lp[i]) - logp) <= 2.0 ** -19, (T, i)
+
+
+def test_tiny_temperatures_beside_neighbouring_logits():
+    """Logits one step below the maximum under temperatures far below the step: the maximum alone."""
+    V = 2000
+    us = torch.tensor([0.0, 0.3, 0.8, 1 - 2.0 ** -24])
+    for top in (100.0, -100.0, 1.0, 3e30, 65537.0):
+        t = torch.tensor(top)
+        x = torch.full((4, V), float(torch.nextafter(t, torch.tensor(-math.inf))))
+        x[:, ::2] = float(torch.nextafter(torch.nextafter(t, torch.tensor(-math.inf)), torch.tensor(-math.inf)))
+        x[:, V - 3] = top
+        step = abs(top) * 2.0 ** -24
+        for T in (step / 40, step / 100, step * 1e-4, step * 1e-8, 1e-30 if top < 1e20 else 1.0, TINY):
+            if T < TINY:
+                continue
+            for kw in (dict(), dict(top_k=V - 1), dict(top_k=50), dict(top_p=0.9), dict(min_p=1e-12)):
+                tok, lp = _sample(x, us, T, **kw)
+                assert tok.tolist() == [V - 3] * 4, (top, T, kw)
+                assert float(lp.abs().max()) <= 2.0 ** -20, (top, T, kw)
+
+
+@pytest.mark.parametrize("V", [64, 5000, 201088])
+@pytest.mark.parametrize("k", [0, 20, 40])
+def test_top_p_among_logits_near_the_smallest_normal_number(V, k):
+    """Temperatures where sixteen bins per power of two pass fp32's range: the exponent's
+    histogram is then too coarse to bracket top-p's border, and the whole order decides."""
+    g = torch.Generator().manual_seed(7 + V)
+    us = torch.tensor([0.0, 0.3, 0.66, 0.7, 0.8, 0.9, 0.99])
+    place = torch.randperm(V, generator=g)[:60]
+    live = place.sort().values                                    # (the rest is -inf and weighs nothing)
+    for T in (1.3e-38, 2e-38, 6e-38):
+        T = float(torch.tensor(T, dtype=torch.float32))
+        x = torch.full((len(us), V), -math.inf)
+        x[:, place] = -(torch.arange(60, dtype=torch.float64) * math.log(1.7) * T).float()
+        for p in (0.6, 0.9, 0.99):
+            p32 = float(torch.tensor(p))
+            tok, lp = _sample(x, us, T, top_k=k, top_p=p)
+            for i in range(len(us)):
+                want, logp, margin = S.sample_row(x[i, live], float(us[i]), T, k, p32)
+                if margin <= 4e-7:
+                    continue
+                assert int(tok[i]) == int(live[want]), (T, p, i)
+                assert abs(float(lp[i]) - logp) <= 2.0 ** -19, (T, p, i)
