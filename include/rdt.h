@@ -431,9 +431,9 @@ RDT_API rdt_status rdt_block_forward_paged(const rdt_config* cfg, const rdt_weig
  * tokens hold less than top_p of their weight; min_p > 0 keeps, of these, those with
  * w_v >= min_p.  The first token of the order always stays.  The result is the first v, by
  * index, at which the running sum of the kept weights exceeds u * their total.  NaN logits take
- * no part.  T <= 0, and rows of nothing but -inf and NaN: the token of rdt_greedy_tokens.  The
- * scalars are checked (T >= 0 and finite, top_k >= 0, 0 < top_p <= 1, 0 <= min_p <= 1); a per-row
- * device array [n] that is not NULL takes the scalar's place, and there T NaN or <= 0 means
+ * no part.  T below 2^-127, and rows of nothing but -inf and NaN: the token of rdt_greedy_tokens.
+ * The scalars are checked (T >= 0 and finite, top_k >= 0, 0 < top_p <= 1, 0 <= min_p <= 1); a per-row
+ * device array [n] that is not NULL takes the scalar's place, and there T NaN or < 0 means
  * greedy, T = +inf that every logit above -inf weighs 1, top_k <= 0 and top_p NaN or >= 1 mean
  * off, top_p <= 0 keeps one token, min_p NaN or <= 0 means off and min_p > 1 is 1. */
 typedef struct {

@@ -7,8 +7,8 @@
 //   min-p: of these, those with w_v >= min_p.
 // The first of the order always stays.  The token drawn is the first v, in the vocabulary's
 // order, at which the running sum of the kept weights exceeds u times their total.
-// NaN logits take no part.  T <= 0, or a row with no weight: the most likely token; an infinite T:
-// every logit above -inf weighs 1.
+// NaN logits take no part.  T below 2^-127 (log2(e) / T is past fp32's range), or a row with no
+// weight: the most likely token; an infinite T: every logit above -inf weighs 1.
 //
 // The exponent (x - m) log2(e) / T is formed in two fp32 words, so a weight is off by about one
 // rounding of its 24 bits wherever it lies.  A thread sums its weights in two fp32 words, in a
@@ -594,7 +594,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_sample(SampleParams p, int ch
   }
   cluster_sync(cl, C);
   mx = warp_max(lane < C ? *cl.map_shared_rank(&sh.mx, lane) : -INFINITY);
-  if (!(T > 0.f) || mx == -INFINITY) {                           // the most likely token
+  if (!(T >= 0x1p-127f) || mx == -INFINITY) {                    // the most likely token
     uint32_t best = 0x7fffffff;
     row.each4([&](const float* x, int l) {
       if (x[0] == mx || x[1] == mx || x[2] == mx || x[3] == mx)

@@ -150,3 +150,25 @@ def test_top_p_among_logits_near_the_smallest_normal_number(V, k):
                     continue
                 assert int(tok[i]) == int(live[want]), (T, p, i)
                 assert abs(float(lp[i]) - logp) <= 2.0 ** -19, (T, p, i)
+
+
+def test_temperatures_around_the_smallest_normal_number():
+    """Below 2^-127 greedy, as 0 is: log2(e) / T is past fp32's range there.  From there on by the
+    definition, among logits that are themselves below the smallest normal number."""
+    V = 700
+    g = torch.Generator().manual_seed(3)
+    us = torch.tensor([0.0, 0.31, 0.5, 0.77, 1 - 2.0 ** -24])
+    f32 = lambda a: float(torch.tensor(a, dtype=torch.float32))
+    for scale in (1e-39, 1e-38, 1e-36, 1.0):
+        x = torch.randn(len(us), V, generator=g) * scale
+        for kw in (dict(), dict(top_k=5), dict(top_p=0.9), dict(min_p=0.1)):
+            for T in (5.8e-39, 4.2e-39, 1e-39, 1e-42, 1.4e-45):
+                tok, lp = _sample(x, us, T, **kw)
+                assert torch.equal(tok.long(), x.argmax(-1)), (scale, T, kw)
+                assert (lp == 0).all()
+            for T in (5.9e-39, 8e-39, 1.1e-38, 1.2e-38, 3e-38):
+                tok, lp = _sample(x, us, T, **kw)
+                for i in range(len(us)):
+                    want, logp, margin = S.sample_row(x[i], float(us[i]), f32(T), kw.get("top_k", 0), f32(kw.get("top_p", 1.0)),
+                                                      f32(kw.get("min_p", 0.0)))
+                    assert margin <= 4e-7 or int(tok[i]) == want, (scale, T, kw, i)
