@@ -19,13 +19,17 @@
 // loads free of bank conflicts.  A weight p enters the second product in two 16-bit words: rows
 // 0-7 hold its upper, rows 8-15 its lower word, which the 8 heads leave free, so p has 16 (bf16)
 // or 22 (fp16) bits at no cost.  e4m3 values become fp16, exactly; a row's exponent of K scales
-// its score, of V its weight, relative to the largest exponent so far.
-//
+// its score, of V its weight.  fp16 ends at 2^-24, so what enters there is p 2^(e - top + 15), e
+// the row's exponent and top the largest so far, under a reference m that is the largest score
+// only while the rows' exponents lie close together: else a row far above the others that no
+// head attends would push the weights of the rest below fp16's range.  Then m is the largest of
+// score + e - top, each head's own, so that what counts most in the sum stands at 2^15 (the
+// weights themselves are fp32 and may pass 1).
 //
 // Measured on one B200 (128 channels; share of the measured copy rate, 6548.5 GB/s): one sequence
 // of 131,071 keys, 32 heads on 8, bf16 98 us (84%); 64 sequences of 1 to 4224 keys, 24 heads on 8,
 // bf16 106 us (80%), bound by HBM with a quarter of the issue slots used; 128 sequences of 4097 to
-// 8191 keys in e4m3 326 us (76%), bound by issue (48% active with 12 warps on an SM).
+// 8191 keys in e4m3 324 us (77%), bound by issue (48% active with 12 warps on an SM).
 //
 // k_paged_attn_simt (fp32 model, other widths): a lane per key and per channel in fp32; 64
 // sequences of 1000 to 2000 keys, 24 heads on 8, in fp32 171 us (70%), in e4m3 281 us (11%).
@@ -212,8 +216,15 @@ template <int PIECES> __device__ __forceinline__ int swz_v(int r, int c) {
 }
 }  // namespace
 
-// 2^d, d <= 0; below the smallest normal value: nothing
+// 2^d, d <= 127; below the smallest normal value: nothing
 __device__ __forceinline__ float pow2_down(int d) { return d < -126 ? 0.f : __int_as_float((127 + d) << 23); }
+// e4m3: a row's weight carries 2^UP, for fp16's upper range (65504).  A tile whose rows' exponents
+// are at most SPREAD below the largest so far, and none above, keeps the score as the reference
+// (its largest weight stands at 2^(UP - SPREAD) or more) and pays one vote for this; 128 sequences
+// of 4097 to 8191 keys 324 us, without 322.  The reference is at most LAG powers of two below the
+// largest score, so that the sum of the weights stays inside fp32.
+constexpr int UP = 15, SPREAD = 8;
+constexpr float LAG = 90.f;
 
 template <int HD, bool Q, bool UNI>
 __global__ void __launch_bounds__(32 * WARPS, HD <= 128 ? Tile<HD, Q>::CTAS : 1) k_paged_attn_mma(PagedAttnParams p, int least) {
@@ -361,10 +372,11 @@ __global__ void __launch_bounds__(32 * WARPS, HD <= 128 ? Tile<HD, Q>::CTAS : 1)
     at.at += u1 - u0;
     if (t0 == t1) continue;
     const int g = seg / n_ht, h0 = seg % n_ht * GT, nh = min(GT, G - h0);
-    float m = -INFINITY, l = 0.f;                     // of head n8; l: this lane's keys
+    float m = -INFINITY, l = 0.f;                     // of head n8: reference, sum of this lane's keys
+    float smax = -INFINITY;                           // e4m3: the largest score up to the last tile that was not close
     float acc[NC][4];                                 // [channel group]: rows n8 (upper words), n8 + 8 (lower)
     uint32_t qf[QR][2];                               // the query's fragments: row n8, columns of the two k8 halves
-    int vexp = -128;                                  // e4m3: acc is in units of 2^vexp
+    int vexp = -128;                                  // e4m3: acc is in units of 2^(vexp - UP)
     float sl2;                                        // scores to base-2 logarithms (and the query's own scale)
     // the query
     {
@@ -434,14 +446,21 @@ __global__ void __launch_bounds__(32 * WARPS, HD <= 128 ? Tile<HD, Q>::CTAS : 1)
           }
         }
         // e4m3: lane r turns its key's exponents into the factors of the score and of the weight
-        float kf = 0.f, vf = 0.f, shrink = 1.f;
+        float kf = 0.f, vf = 0.f;
+        float drop = 0.f, lv = 0.f;
+        bool close = true;                              // the exponents are within SPREAD below the largest before
         if (Q) {
           const bool mine = ok >> lane & 1;
-          const int top = max(vexp, (int)__reduce_max_sync(0xffffffffu, mine ? ve_r[0] - 127 : -128));
+          const int ve = mine ? ve_r[0] - 127 : -128;
           kf = exp_byte_scale(ke_r[0]);
-          vf = mine ? pow2_down(ve_r[0] - 127 - top) : 0.f;
-          shrink = pow2_down(vexp - top);
-          vexp = top;
+          close = !__any_sync(0xffffffffu, mine && (unsigned)(vexp - ve) > (unsigned)SPREAD);
+          if (!close) {
+            const int top = max(vexp, (int)__reduce_max_sync(0xffffffffu, ve));
+            drop = (float)(vexp - top);                 // by how much acc's unit grows
+            vexp = top;
+            lv = (float)(ve - top);
+          }
+          vf = mine ? pow2_down(ve - vexp + UP) : 0.f;
         }
         float mx = -INFINITY;
 #pragma unroll
@@ -464,15 +483,27 @@ __global__ void __launch_bounds__(32 * WARPS, HD <= 128 ? Tile<HD, Q>::CTAS : 1)
         // (a NaN score drops out of the maximum, and its weight makes the sums NaN)
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const float mn = fmaxf(m, mx), base = mn == -INFINITY ? 0.f : mn;
+        float mn = fmaxf(m, mx);
+        if (Q && !close) {
+          smax = fmaxf(fmaxf(smax, m), mx);             // (m: of the tiles since)
+          float mu = -INFINITY;
+#pragma unroll
+          for (int kg = 0; kg < NG; ++kg)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) mu = fmaxf(mu, sc[kg][e] + __shfl_sync(0xffffffffu, lv, kg * 8 + 2 * j4 + e));
+          mu = fmaxf(mu, __shfl_xor_sync(0xffffffffu, mu, 1));
+          mu = fmaxf(mu, __shfl_xor_sync(0xffffffffu, mu, 2));
+          mn = fmaxf(fmaxf(m + drop, mu), smax - LAG);
+        }
+        const float base = mn == -INFINITY ? 0.f : mn;
         const float corr = ex2(m - base);
-        m = mn;
-        if (__any_sync(0xffffffffu, corr != 1.f) || (Q && shrink != 1.f)) {
-          const float f = corr * shrink;
+        if (__any_sync(0xffffffffu, corr != 1.f) || (Q && !close)) {
+          const float f = Q && !close ? ex2(m + drop - base) : corr;
           l *= corr;
 #pragma unroll
           for (int i = 0; i < NC; ++i) acc[i][0] *= f, acc[i][1] *= f, acc[i][2] *= f, acc[i][3] *= f;
         }
+        m = mn;
         uint32_t ph[NG], pl[NG];                        // weights of keys 8 g + 2 j4, + 1
 #pragma unroll
         for (int kg = 0; kg < NG; ++kg) {
@@ -524,7 +555,7 @@ __global__ void __launch_bounds__(32 * WARPS, HD <= 128 ? Tile<HD, Q>::CTAS : 1)
     }
     l += __shfl_xor_sync(0xffffffffu, l, 1);
     l += __shfl_xor_sync(0xffffffffu, l, 2);
-    const float back = Q ? ldexpf(1.f, vexp) : 1.f;
+    const float back = Q ? ldexpf(1.f, vexp) : 1.f, down = Q ? pow2_down(-UP) : 1.f;
     // column n of channel group c is element c % EPP of the piece c / EPP * 8 + n, and this
     // lane has columns 2 j4, + 1 of row n8: whole pieces
     if (t0 == 0 && t1 == nt) {
@@ -539,7 +570,7 @@ __global__ void __launch_bounds__(32 * WARPS, HD <= 128 ? Tile<HD, Q>::CTAS : 1)
             if (ch >= hd) continue;
             bf16 y[EPP];
 #pragma unroll
-            for (int i = 0; i < EPP; ++i) y[i] = from_f<bf16>((acc[h * EPP + i][e] + acc[h * EPP + i][2 + e]) * inv * back);
+            for (int i = 0; i < EPP; ++i) y[i] = from_f<bf16>((acc[h * EPP + i][e] + acc[h * EPP + i][2 + e]) * down * inv * back);
 #pragma unroll
             for (int i = 0; i < EPP; i += 8) {
               uint32_t w[4];
@@ -574,10 +605,10 @@ __global__ void __launch_bounds__(32 * WARPS, HD <= 128 ? Tile<HD, Q>::CTAS : 1)
 #pragma unroll
             for (int i = 0; i < EPP; i += 4) {
               float4 y;
-              y.x = (acc[h * EPP + i][e] + acc[h * EPP + i][2 + e]) * back;
-              y.y = (acc[h * EPP + i + 1][e] + acc[h * EPP + i + 1][2 + e]) * back;
-              y.z = (acc[h * EPP + i + 2][e] + acc[h * EPP + i + 2][2 + e]) * back;
-              y.w = (acc[h * EPP + i + 3][e] + acc[h * EPP + i + 3][2 + e]) * back;
+              y.x = (acc[h * EPP + i][e] + acc[h * EPP + i][2 + e]) * down * back;
+              y.y = (acc[h * EPP + i + 1][e] + acc[h * EPP + i + 1][2 + e]) * down * back;
+              y.z = (acc[h * EPP + i + 2][e] + acc[h * EPP + i + 2][2 + e]) * down * back;
+              y.w = (acc[h * EPP + i + 3][e] + acc[h * EPP + i + 3][2 + e]) * down * back;
               *reinterpret_cast<float4*>(po + ch + i) = y;
             }
           }
