@@ -216,6 +216,10 @@ template <int PIECES> __device__ __forceinline__ int swz_v(int r, int c) {
 }
 }  // namespace
 
+// The sum over the weights' upper words and over their lower ones, which may be 0 or negative: an
+// infinite value is in the upper words' sum as it should be (those are above 0), in the lower
+// words' as a NaN or with the wrong sign.
+__device__ __forceinline__ float both_words(float hi, float lo) { return fabsf(hi) <= 3.402823466e38f ? hi + lo : hi; }
 // 2^d, d <= 127; below the smallest normal value: nothing
 __device__ __forceinline__ float pow2_down(int d) { return d < -126 ? 0.f : __int_as_float((127 + d) << 23); }
 // e4m3: a row's weight carries 2^UP, for fp16's upper range (65504).  A tile whose rows' exponents
@@ -570,7 +574,7 @@ __global__ void __launch_bounds__(32 * WARPS, HD <= 128 ? Tile<HD, Q>::CTAS : 1)
             if (ch >= hd) continue;
             bf16 y[EPP];
 #pragma unroll
-            for (int i = 0; i < EPP; ++i) y[i] = from_f<bf16>((acc[h * EPP + i][e] + acc[h * EPP + i][2 + e]) * down * inv * back);
+            for (int i = 0; i < EPP; ++i) y[i] = from_f<bf16>(both_words(acc[h * EPP + i][e], acc[h * EPP + i][2 + e]) * down * inv * back);
 #pragma unroll
             for (int i = 0; i < EPP; i += 8) {
               uint32_t w[4];
@@ -605,10 +609,10 @@ __global__ void __launch_bounds__(32 * WARPS, HD <= 128 ? Tile<HD, Q>::CTAS : 1)
 #pragma unroll
             for (int i = 0; i < EPP; i += 4) {
               float4 y;
-              y.x = (acc[h * EPP + i][e] + acc[h * EPP + i][2 + e]) * down * back;
-              y.y = (acc[h * EPP + i + 1][e] + acc[h * EPP + i + 1][2 + e]) * down * back;
-              y.z = (acc[h * EPP + i + 2][e] + acc[h * EPP + i + 2][2 + e]) * down * back;
-              y.w = (acc[h * EPP + i + 3][e] + acc[h * EPP + i + 3][2 + e]) * down * back;
+              y.x = both_words(acc[h * EPP + i][e], acc[h * EPP + i][2 + e]) * down * back;
+              y.y = both_words(acc[h * EPP + i + 1][e], acc[h * EPP + i + 1][2 + e]) * down * back;
+              y.z = both_words(acc[h * EPP + i + 2][e], acc[h * EPP + i + 2][2 + e]) * down * back;
+              y.w = both_words(acc[h * EPP + i + 3][e], acc[h * EPP + i + 3][2 + e]) * down * back;
               *reinterpret_cast<float4*>(po + ch + i) = y;
             }
           }

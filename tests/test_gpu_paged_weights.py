@@ -157,3 +157,45 @@ def test_value_rows_of_every_size(dtype, hd, page, shape, n):
     out = R.paged_attention(q[None].cuda(), torch.tensor([n], dtype=torch.int32, device="cuda"), cache)[0]
     ratio, _ = _check(cache, q, n, out)
     assert ratio <= 1.0, ratio
+
+
+@pytest.mark.parametrize("dtype,hd", [("bf16", 128), ("bf16", 64), ("bf16", 256), ("bf16", 40), ("bf16", 33), ("fp32", 64)])
+@pytest.mark.parametrize("n", [1, 20, 2500])
+def test_infinite_keys_and_values(dtype, hd, n):
+    """An infinite value is its channel's output, with its sign, for every head (both signs: NaN; a
+    NaN value: NaN); a key of -inf (against a positive channel of the query) takes no part."""
+    Hkv, G, page = 2, 3, 16
+    g = torch.Generator().manual_seed(n + hd)
+    K = torch.randn(Hkv, n, hd, generator=g)
+    V = torch.randn(Hkv, n, hd, generator=g)
+    q = torch.randn(Hkv * G, hd, generator=g)
+    r = torch.randint(0, n, (4,), generator=g)
+    inf = math.inf
+    V[:, r[0], 3] = inf
+    V[:, r[1], 8] = -inf
+    V[0, r[2], 17] = math.nan
+    if n > 1:
+        V[1, 0, 20] = inf
+        V[1, n - 1, 20] = -inf
+    cache = _cache(K, V, page, dtype, False)
+    q = q.to(cache.torch_dtype)
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    out = R.paged_attention(q[None].cuda(), lens, cache)[0].cpu().reshape(Hkv, G, hd)
+    odd = torch.zeros(Hkv, G, hd, dtype=torch.bool)
+    odd[:, :, [3, 8]] = True
+    odd[0, :, 17] = True
+    if n > 1:
+        odd[1, :, 20] = True
+        assert torch.isnan(out[1, :, 20]).all()
+    assert (out[:, :, 3] == inf).all() and (out[:, :, 8] == -inf).all() and torch.isnan(out[0, :, 17]).all()
+    assert torch.isfinite(out[~odd]).all()
+    plain = V.clone()
+    plain[~torch.isfinite(plain)] = 0.0
+    same = R.paged_attention(q[None].cuda(), lens, _cache(K, plain, page, dtype, False))[0].cpu().reshape(Hkv, G, hd)
+    assert torch.equal(out[~odd], same[~odd])                       # the other channels are as without them
+    if n > 1:
+        q[:, 5] = q[:, 5].abs() + 1
+        K[:, r[3], 5] = -inf
+        cache = _cache(K, plain, page, dtype, False)
+        ratio, _ = _check(cache, q, n, R.paged_attention(q[None].cuda(), lens, cache)[0], without=(int(r[3]),))
+        assert ratio <= 1.0, ratio
