@@ -400,7 +400,8 @@ RDT_API rdt_status rdt_paged_attention(const rdt_paged_cache* cache, int loop, c
  * the call's rows are written to their pages (positions start_pos + t, or cache_len[b]); a
  * decode step attends with rdt_paged_attention's kernel; a prefill at start_pos 0 attends to
  * its own rows as projected, one at start_pos > 0 to positions 0 .. start_pos + seq - 1 read
- * back from the pages.  cache_len and the table are read on the device.  ws:
+ * back from the pages (rows of zeros where a table entry is out of range; the decode step leaves
+ * such positions out).  cache_len and the table are read on the device.  ws:
  * rdt_paged_workspace_size bytes for the call's batch, seq and start_pos (0 for a decode step),
  * used as any other workspace; its first bytes are the call's status word. */
 RDT_API size_t rdt_paged_workspace_size(const rdt_config* cfg, int batch, int seq, int start_pos,

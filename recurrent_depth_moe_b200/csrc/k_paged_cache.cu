@@ -3,7 +3,8 @@
 // write: row i = b * seq + t of k and v goes to slot pos % page_size of page
 //   table[b][pos / page_size], every kv head as one row of head_dim values, in the model dtype
 //   or as e4m3 with one exponent byte (paged.cuh).  pos < 0: a padding row, nothing written.
-// read: positions 0 .. lens[b] - 1 of every sequence, contiguous, in the model dtype.
+// read: positions 0 .. lens[b] - 1 of every sequence, contiguous, in the model dtype; a position
+//   whose page is out of range stays as it was, or (for a caller that reads all rows) becomes zeros.
 // Both move each byte once, so they are HBM-bound: a lane moves 16 bytes of the wider side at a
 // time, and a thread has several rows of K and V in flight.  Widths or addresses that 16-byte
 // pieces do not divide go value by value.  Measured on one B200: 16,384 rows of 8 heads of 128
@@ -156,13 +157,15 @@ __global__ void __launch_bounds__(NT) k_paged_read(PagedReadParams p) {
   const int n = min(visible_keys(p.c, p.lens, b, p.len_add, p.st, 211), p.t_out);
   if (t >= n) return;
   const int page = page_of(p.c, b, t, p.st, 212);
-  if (page < 0) return;
+  if (page < 0 && !p.zero_bad) return;
   const long long slot = ((long long)page * Hkv + g) * p.c.page_size + slot_of(p.c, t);
   const long long out = (((long long)b * Hkv + g) * p.t_out + t) * hd;
 #pragma unroll
   for (int kv = 0; kv < 2; ++kv) {
     T* dst = (T*)(kv ? p.v_out : p.k_out) + out;
-    if (!Q) {
+    if (page < 0) {
+      for (int d = lane; d < hd; d += 32) dst[d] = from_f<T>(0.f);
+    } else if (!Q) {
       const T* src = (const T*)(kv ? p.c.v : p.c.k) + slot * hd;
       for (int d = lane; d < hd; d += 32) dst[d] = src[d];
     } else {
@@ -190,6 +193,7 @@ __global__ void __launch_bounds__(NT) k_paged_read_vec(PagedReadParams p, int rt
     if (t < n) {
       const int page = page_of(p.c, b, t, p.st, 212);
       if (page >= 0) s = ((long long)page * Hkv + g) * p.c.page_size + slot_of(p.c, t);
+      else if (p.zero_bad) s = -2;
     }
     slot_s[tid] = s;
     if (Q && s >= 0) sc[0][tid] = exp_byte_scale(__ldg(p.c.ke + s)), sc[1][tid] = exp_byte_scale(__ldg(p.c.ve + s));
@@ -199,11 +203,11 @@ __global__ void __launch_bounds__(NT) k_paged_read_vec(PagedReadParams p, int rt
   const long long out = (((long long)b * Hkv + g) * p.t_out + t0) * hd;
   for (int i0 = tid; i0 < pieces; i0 += NT * UN) {
     uint4 w[2][UN];
-    int at[UN];                                              // row of the piece, -1: nothing to copy
+    int at[UN];                                              // row of the piece, -1: nothing to copy, -2: zeros
 #pragma unroll
     for (int u = 0; u < UN; ++u) {
       const int i = i0 + u * NT, r = i / per, d = (i - r * per) * N;
-      at[u] = i < pieces && slot_s[r] >= 0 ? r : -1;
+      at[u] = i >= pieces ? -1 : slot_s[r] >= 0 ? r : (int)slot_s[r];
       if (at[u] < 0) continue;
       const long long s = slot_s[r] * hd + d;
 #pragma unroll
@@ -218,12 +222,12 @@ __global__ void __launch_bounds__(NT) k_paged_read_vec(PagedReadParams p, int rt
     }
 #pragma unroll
     for (int u = 0; u < UN; ++u) {
-      if (at[u] < 0) continue;
+      if (at[u] == -1) continue;
       const int i = i0 + u * NT;
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv) {
-        uint4 y = w[kv][u];
-        if (Q) {
+        uint4 y = at[u] < 0 ? make_uint4(0, 0, 0, 0) : w[kv][u];
+        if (Q && at[u] >= 0) {
           const float f = sc[kv][at[u]];
           const uint32_t q[2] = {y.x, y.y};
           float x[N];

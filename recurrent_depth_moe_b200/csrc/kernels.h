@@ -272,6 +272,7 @@ struct PagedReadParams {
   const int* lens; int len_add;                 // positions 0 .. lens[b] (0 without lens) + len_add - 1
   int B, t_out;
   void* k_out; void* v_out;                     // [B][Hkv][t_out][hd] model dtype
+  int zero_bad;                                 // positions of a bad page: zeros (else: left as they were)
   DevStatus* st;
 };
 struct PagedAttnParams {

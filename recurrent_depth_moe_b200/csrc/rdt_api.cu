@@ -306,6 +306,7 @@ rdt_status attention_block(Ctx& x, int B, int T, const float* combined, const vo
         memset(&pr, 0, sizeof(pr));
         pr.c = paged_view(x.paged, loop_t);
         pr.len_add = keys; pr.B = B; pr.t_out = keys;
+        pr.zero_bad = 1;                    // every position is attended to
         pr.k_out = at<void*>(x.ws, x.paged_off);
         pr.v_out = (char*)pr.k_out + align256((size_t)B * Hkv * keys * hd * es);
         pr.st = x.st;
