@@ -364,6 +364,8 @@ typedef struct {
   int n_loops, n_pages, page_size;
   int n_kv_heads, head_dim;   /* head_dim <= 256                                         */
   int batch, max_pages;       /* table rows, entries of one row                          */
+  void* status;               /* NULL, or a 16-byte device status word (as `status` below) in  */
+                              /* which every call over the cache records, beside the call's own */
 } rdt_paged_cache;
 
 /* Write n_rows rows of keys and values (model dtype; row i, kv head g at i * row_ld +
@@ -403,7 +405,8 @@ RDT_API rdt_status rdt_paged_attention(const rdt_paged_cache* cache, int loop, c
  * back from the pages (rows of zeros where a table entry is out of range; the decode step leaves
  * such positions out).  cache_len and the table are read on the device.  ws:
  * rdt_paged_workspace_size bytes for the call's batch, seq and start_pos (0 for a decode step),
- * used as any other workspace; its first bytes are the call's status word. */
+ * used as any other workspace; its first bytes are the call's status word (of the latest call
+ * alone; the cache's own keeps what was recorded until it is read). */
 RDT_API size_t rdt_paged_workspace_size(const rdt_config* cfg, int batch, int seq, int start_pos,
                                         const rdt_paged_cache* cache);
 RDT_API rdt_status rdt_recurrent_forward_paged(const rdt_config* cfg, const rdt_weights* w, const float* h0,

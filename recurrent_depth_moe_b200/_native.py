@@ -63,7 +63,7 @@ class rdt_paged_cache(ctypes.Structure):
     _fields_ = [("k", c_void_p), ("v", c_void_p), ("k_exp", c_void_p), ("v_exp", c_void_p),
                 ("page_table", c_void_p)] + [(n, c_int) for n in (
                     "dtype", "kv_type", "n_loops", "n_pages", "page_size", "n_kv_heads", "head_dim", "batch",
-                    "max_pages")]
+                    "max_pages")] + [("status", c_void_p)]
 
 
 class rdt_sampling(ctypes.Structure):

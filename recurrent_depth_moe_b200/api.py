@@ -664,6 +664,8 @@ class Generator:
         self.ws_rec_decode = self.rb.workspace(B, 1, self.t_max, cache=paged)
         cs = config_struct(cfg)
         self.ws_head = alloc_workspace(workspace_size(cs, 1, B, B))
+        for ws in (self.ws_block, self.ws_rec_prefill, self.ws_rec_decode):
+            ws[:16].zero_()                                                     # (read_status before any call)
         V = MW["head"].shape[0]
         dt = _DT[cfg.dtype][1]
         self.xa = torch.empty(B * T0, D, dtype=torch.float32, device="cuda")
@@ -763,6 +765,16 @@ class Generator:
         self._graph.replay()
         self.tokens[step].copy_(self.cur_tok)
         return self.tokens[step]
+
+    def read_status(self) -> int:
+        """Synchronise, read and clear the status words of the paged caches; without them, those of
+        the latest calls.  The first error, or RDT_OK."""
+        if isinstance(self.rec_cache, PagedKVCache):
+            codes = [c.read_status() for c in self.pre_cache + [self.rec_cache] + self.coda_cache]
+        else:
+            codes = [N.load().rdt_read_device_status(ws.data_ptr(), _stream())
+                     for ws in (self.ws_block, self.ws_rec_prefill, self.ws_rec_decode)]
+        return next((c for c in codes if c != N.RDT_OK), N.RDT_OK)
 
     def run(self, prompt_ids: torch.Tensor, u: Optional[torch.Tensor] = None) -> torch.Tensor:
         """Prompt [B, T0] -> the generated tokens [B, max_new_tokens] (int32, CUDA).  u: uniform

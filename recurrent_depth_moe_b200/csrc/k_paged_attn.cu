@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(32 * WARPS, HD <= 128 ? Tile<HD, Q>::CTAS : 1)
     const int pi = page_index(p.c, key);
     const int page = __ldg(table + pi);
     if ((unsigned)page >= (unsigned)p.c.n_pages) {
-      record_status(p.st, ST_BOUNDS, 222, page);
+      record_bad(p.c, p.st, 222, page);
       return -1;
     }
     return ((long long)page * Hkv + ig) * ps + (key - pi * ps);

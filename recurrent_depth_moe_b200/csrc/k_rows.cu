@@ -56,12 +56,13 @@ __global__ void k_positions(int* pos, int N, int seq, int start_pos) {
 
 // decode: the new token of sequence b sits at cache_len[b]; out-of-range lengths are
 // recorded in the status word and clamped so no table or cache access leaves its buffer.
-__global__ void k_positions_decode(int* pos, const int* cache_len, int B, int t_max, DevStatus* st) {
+__global__ void k_positions_decode(int* pos, const int* cache_len, int B, int t_max, DevStatus* st, DevStatus* also) {
   int r = blockIdx.x * blockDim.x + threadIdx.x;
   if (r >= B) return;
   int p = cache_len[r];
   if (p < 0 || p >= t_max) {
     record_status(st, ST_BOUNDS, 102, p);
+    record_status(also, ST_BOUNDS, 102, p);
     p = p < 0 ? 0 : t_max - 1;
   }
   pos[r] = p;
@@ -381,8 +382,9 @@ void launch_rope_table(float2* tab, int n_pos, int dim, float theta, cudaStream_
 void launch_positions(int* pos, int N, int seq, int start_pos, cudaStream_t s) {
   { k_positions<<<(N + 255) / 256, 256, 0, s>>>(pos, N, seq, start_pos); note_launch(); }
 }
-void launch_positions_decode(int* pos, const int* cache_len, int B, int t_max, DevStatus* st, cudaStream_t s) {
-  { k_positions_decode<<<(B + 255) / 256, 256, 0, s>>>(pos, cache_len, B, t_max, st); note_launch(); }
+void launch_positions_decode(int* pos, const int* cache_len, int B, int t_max, DevStatus* st, cudaStream_t s,
+                             DevStatus* also) {
+  { k_positions_decode<<<(B + 255) / 256, 256, 0, s>>>(pos, cache_len, B, t_max, st, also); note_launch(); }
 }
 void launch_loop_prologue(int dtype, const float* h, const void* e, const float* emb, int loop_dim,
                           const float* w_rec, const float* w_attn, float* combined, void* a,

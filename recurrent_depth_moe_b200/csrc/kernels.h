@@ -209,7 +209,8 @@ void launch_lti_A(const float* log_A, const float* log_dt, float* A, int D, cuda
 void launch_loop_emb(float* emb, int loop_dim, int t, float theta, cudaStream_t s);
 void launch_rope_table(float2* tab, int n_pos, int dim, float theta, cudaStream_t s);
 void launch_positions(int* pos, int N, int seq, int start_pos, cudaStream_t s);
-void launch_positions_decode(int* pos, const int* cache_len, int B, int t_max, DevStatus* st, cudaStream_t s);
+void launch_positions_decode(int* pos, const int* cache_len, int B, int t_max, DevStatus* st, cudaStream_t s,
+                             DevStatus* also = nullptr);   // also: a second status word
 // row_loop (optional): row r adds the loop embedding emb + max(row_loop[r], 0) * emb_stride
 void launch_loop_prologue(int dtype, const float* h, const void* e, const float* emb, int loop_dim,
                           const float* w_rec, const float* w_attn, float* combined, void* a,
@@ -259,6 +260,7 @@ struct PagedView {
   const int* table;
   int e4m3, n_pages, page_size, Hkv, hd, max_pages;
   int ps_shift;                  // page_size is 1 << ps_shift, or -1
+  DevStatus* also;               // the cache's own status word beside the call's, or null
 };
 struct PagedWriteParams {
   PagedView c;

@@ -48,21 +48,26 @@ __device__ __forceinline__ float e4m3_f(uint8_t q) {
   return __half2float(__half(__nv_cvt_fp8_to_halfraw(q, __NV_E4M3)));
 }
 
+// An index out of range: in the call's status word and in the cache's.
+__device__ __forceinline__ void record_bad(const PagedView& c, DevStatus* st, int where, int detail) {
+  record_status(st, ST_BOUNDS, where, detail);
+  record_status(c.also, ST_BOUNDS, where, detail);
+}
 // Which page of its sequence a position is in.
 __device__ __forceinline__ int page_index(const PagedView& c, int pos) {
   return c.ps_shift >= 0 ? pos >> c.ps_shift : pos / c.page_size;
 }
-// Page of position pos of sequence b, or -1 (recorded in the status word) if the position or
+// Page of position pos of sequence b, or -1 (recorded) if the position or
 // the table's entry is out of range.
 __device__ __forceinline__ int page_of(const PagedView& c, int b, int pos, DevStatus* st, int where) {
   const int pi = page_index(c, pos);
   if (pos < 0 || pi >= c.max_pages) {
-    record_status(st, ST_BOUNDS, where, pos);
+    record_bad(c, st, where, pos);
     return -1;
   }
   const int page = __ldg(c.table + (long long)b * c.max_pages + pi);
   if (page < 0 || page >= c.n_pages) {
-    record_status(st, ST_BOUNDS, where + 1, page);
+    record_bad(c, st, where + 1, page);
     return -1;
   }
   return page;
@@ -74,7 +79,7 @@ __device__ __forceinline__ int visible_keys(const PagedView& c, const int* lens,
   const int n = (lens ? __ldg(lens + b) : 0) + len_add;
   const long long cap = (long long)c.max_pages * c.page_size;
   if (n > cap) {
-    record_status(st, ST_BOUNDS, where, n);
+    record_bad(c, st, where, n);
     return (int)cap;
   }
   return n > 0 ? n : 0;

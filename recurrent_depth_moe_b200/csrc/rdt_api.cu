@@ -610,7 +610,8 @@ rdt_status run_recurrent(const rdt_config* c, const rdt_weights* w, const float*
   if (cudaMemsetAsync(at<void*>(ws, x.L.halted), 0, (size_t)N * 4, s) != cudaSuccess) return RDT_ERR_CUDA;
   launch_lti_A(w->log_A, w->log_dt, at<float*>(ws, x.L.Avec), D, s);
   launch_rope_table(at<float2*>(ws, x.L.rope), x.L.rope_pos, x.L.rope_dim, c->rope_theta, s);
-  if (decode) launch_positions_decode(pos, cache_len, B, paged ? paged->max_pages * paged->page_size : cache->t_max, x.st, s);
+  if (decode) launch_positions_decode(pos, cache_len, B, paged ? paged->max_pages * paged->page_size : cache->t_max, x.st, s,
+                                      paged ? (DevStatus*)paged->status : nullptr);
   else launch_positions(pos, N, T, start_pos, s);
   launch_iota(at<int*>(ws, x.L.run_list), at<int*>(ws, x.L.run_idx), at<int*>(ws, x.L.nrun), N, s);
   CombineParams cp = combine_base(x, N);
@@ -944,7 +945,8 @@ static rdt_status block_forward(const rdt_config* cfg, const rdt_weights* w, con
   if (cudaMemsetAsync(x.st, 0, sizeof(DevStatus), s) != cudaSuccess) return RDT_ERR_CUDA;
   launch_rope_table(at<float2*>(ws, x.L.rope), x.L.rope_pos, x.L.rope_dim, cfg->rope_theta, s);
   if (decode) launch_positions_decode(at<int*>(ws, x.L.pos), cache_len, batch,
-                                      paged ? paged->max_pages * paged->page_size : cache->t_max, x.st, s);
+                                      paged ? paged->max_pages * paged->page_size : cache->t_max, x.st, s,
+                                      paged ? (DevStatus*)paged->status : nullptr);
   else launch_positions(at<int*>(ws, x.L.pos), N, seq, start_pos, s);
   void* a = at<void*>(ws, x.L.a);
   float* x1 = at<float*>(ws, x.L.x1);

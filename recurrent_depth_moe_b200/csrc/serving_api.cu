@@ -37,6 +37,7 @@ PagedView paged_view(const rdt_paged_cache* c, int loop) {
   v.e4m3 = c->kv_type;
   v.n_pages = c->n_pages; v.page_size = c->page_size; v.Hkv = c->n_kv_heads; v.hd = c->head_dim;
   v.max_pages = c->max_pages;
+  v.also = (DevStatus*)c->status;
   v.ps_shift = -1;
   for (int i = 0; i < 31; ++i)
     if (c->page_size == 1 << i) v.ps_shift = i;

@@ -79,8 +79,8 @@ class PagedKVCache:
     ("fp32" | "bf16") is the model dtype, needed for an e4m3 cache.  page_table int32
     [batch, max_pages]: position t of sequence b is slot t % page_size of page
     page_table[b, t // page_size].  The tensors are the caller's; the table may be changed in
-    place between calls.  Out-of-range table entries and positions are recorded in a status word
-    (read_status)."""
+    place between calls.  Out-of-range table entries and positions, in these calls and in the
+    model's over the cache, are recorded in a status word (read_status)."""
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor,
                  k_exp: Optional[torch.Tensor] = None, v_exp: Optional[torch.Tensor] = None,
@@ -116,10 +116,10 @@ class PagedKVCache:
         s.dtype, s.kv_type = _DT[dtype][0], int(quant)
         s.n_loops, s.n_pages, s.page_size = self.n_loops, self.n_pages, self.page_size
         s.n_kv_heads, s.head_dim, s.batch, s.max_pages = self.n_kv_heads, self.head_dim, self.batch, self.max_pages
+        self.status = torch.zeros(4, dtype=torch.int32, device=dev)
+        self._status = s.status = self.status.data_ptr()
         self._struct = s
         self._ref = ctypes.byref(s)
-        self.status = torch.zeros(4, dtype=torch.int32, device=dev)
-        self._status = self.status.data_ptr()
 
     k = property(lambda self: self._k)
     v = property(lambda self: self._v)

@@ -40,6 +40,68 @@ def _paged(cfg, loops, B, t_max, page, quantised=False, seed=0):
     return R.PagedKVCache.alloc(cfg, loops, B, t_max, page, quantised, n_pages=B * per + 3, page_table=_table(B, per, seed))
 
 
+@pytest.mark.parametrize("quantised", [False, True])
+def test_bad_pages_and_positions_reach_the_caches_status(quantised):
+    """Prefill, chunk, decode step, replayed decode step and looped block: a bad table entry, and a
+    length out of range, are in the cache's status word (and, as ever, in the call's workspace),
+    until it is read."""
+    cfg = _cfg("bf16")
+    B, T = 2, 20
+    blk = R.Block(cfg, to_dev(RI.dense_block_weights(cfg, 5)))
+    cache = _paged(cfg, 1, B, 48, 16, quantised)
+    x = torch.randn(B * T, cfg.dim, generator=torch.Generator().manual_seed(6)).cuda()
+    row = x[:B].contiguous()
+    clen = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    ws = blk.workspace(B, T, 48, T, cache)
+    good = cache.page_table.clone()
+    calls = dict(prefill=lambda: blk.forward(x, B, T, 0, cache=cache, workspace=ws),
+                 chunk=lambda: blk.forward(x, B, T, T, cache=cache, workspace=ws),
+                 decode=lambda: blk.forward(row, B, 1, 0, cache=cache, cache_len=clen(30, 17)))
+    for name, call in calls.items():
+        call()
+        assert cache.read_status() == 0, name
+        for bad in (-1, cache.n_pages, 1 << 30):
+            cache.page_table[1, 1] = bad
+            call()
+            cache.page_table.copy_(good)
+            call()                                                    # a good call does not clear the record
+            assert cache.read_status() == BOUNDS, (name, bad)
+            assert cache.read_status() == 0, (name, bad)
+    for bad in (-1, 48, 1 << 30):
+        blk.forward(row, B, 1, 0, cache=cache, cache_len=clen(3, bad))
+        assert cache.read_status() == BOUNDS, bad
+    rec = R.RecurrentBlock(cfg, to_dev(RI.block_weights(cfg, 21, attn_std=0.08)))
+    loops = _paged(cfg, 2, B, 48, 16, quantised)
+    h, e = row, row.to(torch.bfloat16)
+    good = loops.page_table.clone()
+    dg = R.DecodeGraph(rec, B, loops, clen(20, 20), 2)
+    for i in range(4):                                                # eager, captured, replayed
+        dg.step(h, e)
+        assert loops.read_status() == 0, i
+    loops.page_table[0, 1] = -5
+    dg.step(h, e)
+    assert rec.read_status() == BOUNDS and loops.read_status() == BOUNDS
+    loops.page_table.copy_(good)
+    dg.step(h, e)
+    assert rec.read_status() == 0 and loops.read_status() == 0
+
+
+def test_the_generators_status():
+    wl = RI.get_workload("tiny_gqa_fp32")
+    MW = to_dev(RI.model_weights(wl.cfg, wl.seed))
+    ids = torch.randint(0, wl.cfg.vocab_size, (2, 16), generator=torch.Generator().manual_seed(31)).int().cuda()
+    for kw in (dict(), dict(page_size=8)):
+        gen = R.Generator(wl.cfg, MW, 2, 16, 4, 4, **kw)
+        gen.run(ids)
+        assert gen.read_status() == 0
+    for cache in (gen.pre_cache[0], gen.rec_cache, gen.coda_cache[0]):
+        good = cache.page_table.clone()
+        cache.page_table[1, 0] = 99
+        gen.run(ids)
+        cache.page_table.copy_(good)
+        assert gen.read_status() == BOUNDS and gen.read_status() == 0
+
+
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 @pytest.mark.parametrize("quantised", [False, True])
 @pytest.mark.parametrize("page", [16, 5])
@@ -61,10 +123,12 @@ def test_prefill_behind_unreadable_pages_is_of_this_call_alone(dtype, quantised,
         ws.fill_(fill)
         ws[:16] = 0
         outs.append(blk.forward(y, B, T, T, cache=cache, workspace=ws).clone())
+        assert cache.read_status() == BOUNDS
         cache.page_table[1, 0] = page1
     assert torch.isfinite(outs[0]).all()
     assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
     for t in (cache.k, cache.v):
         t[:, page1].zero_()
     want = blk.forward(y, B, T, T, cache=cache, workspace=ws)
+    assert cache.read_status() == 0
     assert torch.equal(outs[0], want)
