@@ -614,6 +614,10 @@ class Sampling:
     min_p: Union[float, torch.Tensor] = 0.0
 
 
+def _parameters(s: Optional[Sampling]) -> tuple:
+    return () if s is None else (s.temperature, s.top_k, s.top_p, s.min_p)
+
+
 class Generator:
     """OpenMythos.generate on the library's entry points ("OpenMythos 분석", RoPE &
     generation cache): step 0 runs the whole prompt at start_pos 0 and fills one cache per
@@ -628,7 +632,9 @@ class Generator:
     prelude, coda, head and greedy choice) are captured once into a CUDA graph on the
     second decode call and replayed from then on.  Everything a step reads is at a fixed
     address: the previous token is copied into `cur_tok` and the cache length set before
-    the replay, and the new token copied out of `cur_tok` after it.  The first decode call
+    the replay, and the new token copied out of `cur_tok` after it.  When `sampling` is given
+    other numbers or tensors the step is captured anew; a tensor's values may change in place.
+    The first decode call
     runs eagerly (it also performs the kernels' one-time attribute setup), and so does every
     call made while the library's profiler is recording."""
 
@@ -687,6 +693,7 @@ class Generator:
         self.trace_prefill = Trace.alloc(cfg, n_loops, 0, B * T0) if trace else None
         self.trace_decode = Trace.alloc(cfg, n_loops, 0, B) if trace else None
         self._graph = None
+        self._graph_sampling = None  # the parameters that the captured step holds
         self._eager_decodes = 0
         self.graph_launches = 0      # library kernels in one replay of the captured step
 
@@ -725,6 +732,15 @@ class Generator:
             s = self.sampling
             sample_tokens(self.logits, self.u_in, s.temperature, s.top_k, s.top_p, s.min_p, out=tok_out)
 
+    def _graph_holds(self) -> bool:
+        """Whether the captured step draws with the present parameters: numbers are part of the
+        capture, tensors are read when it replays."""
+        if self._graph is None:
+            return False
+        a, b = self._graph_sampling, _parameters(self.sampling)
+        return len(a) == len(b) and all(
+            x is y or not (isinstance(x, torch.Tensor) or isinstance(y, torch.Tensor)) and x == y for x, y in zip(a, b))
+
     def _decode_body(self, tok_in: torch.Tensor, tok_out: torch.Tensor):
         """One decode step from the tokens in tok_in [B] to the next tokens in tok_out [B],
         with the cache length already in self.cache_len."""
@@ -753,7 +769,7 @@ class Generator:
             self._eager_decodes += 1
             return self.tokens[step]
         self.cur_tok.copy_(self.tokens[step - 1])
-        if self._graph is None:
+        if not self._graph_holds():
             g = torch.cuda.CUDAGraph()
             n0 = N.launch_count()
             # thread-local capture: other threads of the process (a collective library's
@@ -761,7 +777,7 @@ class Generator:
             with torch.cuda.graph(g, capture_error_mode="thread_local"):
                 self._decode_body(self.cur_tok, self.cur_tok)
             self.graph_launches = N.launch_count() - n0
-            self._graph = g
+            self._graph, self._graph_sampling = g, _parameters(self.sampling)
         self._graph.replay()
         self.tokens[step].copy_(self.cur_tok)
         return self.tokens[step]

@@ -132,3 +132,32 @@ def test_prefill_behind_unreadable_pages_is_of_this_call_alone(dtype, quantised,
     want = blk.forward(y, B, T, T, cache=cache, workspace=ws)
     assert cache.read_status() == 0
     assert torch.equal(outs[0], want)
+
+
+def test_sampling_changed_between_generations():
+    """A generator whose parameters are changed draws with the new ones, replayed or not; values
+    changed inside a parameter's tensor count at once."""
+    wl = RI.get_workload("tiny_gqa_fp32")
+    MW = to_dev(RI.model_weights(wl.cfg, wl.seed))
+    ids = torch.randint(0, wl.cfg.vocab_size, (2, 16), generator=torch.Generator().manual_seed(41)).int().cuda()
+    u = torch.rand(8, 2, generator=torch.Generator().manual_seed(42)).cuda()
+    rows = torch.tensor([0.5, 2.0], device="cuda")
+    plans = [R.Sampling(temperature=1.5), R.Sampling(temperature=1.5, top_k=3), R.Sampling(temperature=rows),
+             R.Sampling(temperature=rows.clone() * 3, top_p=0.9), R.Sampling(temperature=0.0)]
+    gen = R.Generator(wl.cfg, MW, 2, 16, 8, 4, sampling=plans[0])
+    seen = []
+    for plan in plans + plans[:1]:
+        want = R.generate(wl.cfg, MW, ids, 8, 4, sampling=plan, u=u)[:, 16:]
+        gen.sampling = plan
+        assert torch.equal(gen.run(ids, u), want)
+        assert torch.equal(gen.run(ids, u), want)
+        seen.append(want.clone())
+    assert any(not torch.equal(a, seen[0]) for a in seen[1:])
+    gen.sampling.temperature = 0.7                                    # in place
+    assert torch.equal(gen.run(ids, u), R.generate(wl.cfg, MW, ids, 8, 4, sampling=R.Sampling(temperature=0.7), u=u)[:, 16:])
+    gen.sampling = plans[2]
+    gen.run(ids, u)
+    rows.fill_(1.1)
+    assert torch.equal(gen.run(ids, u), R.generate(wl.cfg, MW, ids, 8, 4, sampling=R.Sampling(temperature=1.1), u=u)[:, 16:])
+    gen.sampling = None
+    assert torch.equal(gen.run(ids), R.generate(wl.cfg, MW, ids, 8, 4)[:, 16:])
