@@ -720,9 +720,13 @@ class Generator:
                         workspace=self.ws_rec_prefill, trace=self.trace_prefill)
         x, y = self._run_blocks(self.coda, self.coda_cache, self.rec_out[0], y, T0, 0, None)
         head(self.cfg, x, self.MW["norm_w"], self.MW["head"], last_of=T0, out=self.logits, workspace=self.ws_head)
-        self.u_in.copy_(self.u[0])
+        self._take_u(0)
         self._choose(self.tokens[0])
         return self.tokens[0]
+
+    def _take_u(self, step: int):
+        if self.sampling is not None:
+            self.u_in.copy_(self.u[step])
 
     def _choose(self, tok_out: torch.Tensor):
         """The next tokens from self.logits (and the uniform numbers in self.u_in)."""
@@ -763,7 +767,7 @@ class Generator:
     def decode(self, step: int) -> torch.Tensor:
         """Step `step` >= 1: the token of step - 1 at position prompt_len + step - 1."""
         self.cache_len.fill_(self.T0 + step - 1)
-        self.u_in.copy_(self.u[step])
+        self._take_u(step)
         if not self.cuda_graph or N.profiling() or self._eager_decodes == 0:
             self._decode_body(self.tokens[step - 1], self.tokens[step])
             self._eager_decodes += 1

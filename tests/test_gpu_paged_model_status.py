@@ -161,3 +161,13 @@ def test_sampling_changed_between_generations():
     assert torch.equal(gen.run(ids, u), R.generate(wl.cfg, MW, ids, 8, 4, sampling=R.Sampling(temperature=1.1), u=u)[:, 16:])
     gen.sampling = None
     assert torch.equal(gen.run(ids), R.generate(wl.cfg, MW, ids, 8, 4)[:, 16:])
+
+
+def test_greedy_generation_reads_no_uniform_numbers():
+    wl = RI.get_workload("tiny_gqa_fp32")
+    MW = to_dev(RI.model_weights(wl.cfg, wl.seed))
+    ids = torch.randint(0, wl.cfg.vocab_size, (2, 16), generator=torch.Generator().manual_seed(31)).int().cuda()
+    want = R.Generator(wl.cfg, MW, 2, 16, 4, 4).run(ids)
+    gen = R.Generator(wl.cfg, MW, 2, 16, 4, 4)
+    gen.u = gen.u_in = None
+    assert torch.equal(gen.run(ids), want)
