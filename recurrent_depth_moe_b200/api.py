@@ -363,8 +363,8 @@ class DepthBatch:
     each decode n_tokens tokens in order, one slot per sequence; every tick runs the shared
     block once over all slots, each slot's token at its own loop, and a token that halts
     leaves its slot to the sequence's next token (after its remaining loops' keys / values
-    are written from its frozen state).  Results equal n_tokens successive decode_step calls
-    per sequence.  h0 [B, S, D] fp32, e [B, S, D] model dtype, cache_len [B] int32 (position
+    are written from its frozen state).  The caches are contiguous (KVCache).  Results equal
+    n_tokens successive decode_step calls per sequence.  h0 [B, S, D] fp32, e [B, S, D] model dtype, cache_len [B] int32 (position
     of token 0), halt_logit_offset [B, S] fp32 or None.  Outputs: h_out [B, S, D],
     halt_weights [B, S, L], expert_ids [B, S, L, k]."""
 
@@ -372,6 +372,8 @@ class DepthBatch:
                  cache: KVCache, n_loops: int, act_threshold: float = 0.0,
                  halt_logit_offset: Optional[torch.Tensor] = None, out: Optional[tuple] = None,
                  workspace: Optional[torch.Tensor] = None):
+        if isinstance(cache, PagedKVCache):
+            raise ValueError("cache: depth-wise batching takes contiguous caches (KVCache), not paged ones")
         lib = N.load()
         cfg = blk.cfg
         B, S = h0.shape[0], h0.shape[1]

@@ -163,6 +163,15 @@ def test_sampling_changed_between_generations():
     assert torch.equal(gen.run(ids), R.generate(wl.cfg, MW, ids, 8, 4)[:, 16:])
 
 
+def test_depth_batch_refuses_pages():
+    cfg = _cfg("bf16")
+    blk = R.RecurrentBlock(cfg, to_dev(RI.block_weights(cfg, 51)))
+    h0 = torch.zeros(2, 3, cfg.dim, device="cuda")
+    with pytest.raises(ValueError, match="paged"):
+        R.DepthBatch(blk, h0, h0.to(torch.bfloat16), torch.zeros(2, dtype=torch.int32, device="cuda"),
+                     _paged(cfg, 2, 2, 32, 16), 2)
+
+
 def test_greedy_generation_reads_no_uniform_numbers():
     wl = RI.get_workload("tiny_gqa_fp32")
     MW = to_dev(RI.model_weights(wl.cfg, wl.seed))
