@@ -264,7 +264,8 @@ def sample_tokens(logits: torch.Tensor, u: torch.Tensor, temperature: Union[floa
             _check(val, name, torch.int32 if i == 1 else torch.float32, shape, dev)
             rows[i] = val.data_ptr()
         else:
-            scalars[i] = val
+            # (a top_k beyond 32 bits is beyond every vocabulary; below 0 it is refused)
+            scalars[i] = max(-1, min(val, 2 ** 31 - 1)) if i == 1 else val
     a = N.rdt_sampling(*scalars, *rows)
     if out is None:
         out = torch.empty(n, dtype=torch.int32, device=dev)

@@ -172,3 +172,15 @@ def test_temperatures_around_the_smallest_normal_number():
                     want, logp, margin = S.sample_row(x[i], float(us[i]), f32(T), kw.get("top_k", 0), f32(kw.get("top_p", 1.0)),
                                                       f32(kw.get("min_p", 0.0)))
                     assert margin <= 4e-7 or int(tok[i]) == want, (scale, T, kw, i)
+
+
+def test_top_k_of_any_integer():
+    """A top_k beyond 32 bits is beyond every vocabulary: off; a negative one is refused."""
+    x = torch.randn(5, 300, generator=torch.Generator().manual_seed(1)).cuda()
+    u = torch.rand(5, generator=torch.Generator().manual_seed(2)).cuda()
+    want = R.sample_tokens(x, u)
+    for k in (300, 2 ** 31 - 1, 2 ** 31, 2 ** 32 + 1, 2 ** 63 - 1):
+        assert torch.equal(R.sample_tokens(x, u, top_k=k), want), k
+    for k in (-1, -2 ** 32, -2 ** 40):
+        with pytest.raises(R.RdtError):
+            R.sample_tokens(x, u, top_k=k)
