@@ -134,6 +134,48 @@ def test_prefill_behind_unreadable_pages_is_of_this_call_alone(dtype, quantised,
     assert torch.equal(outs[0], want)
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("act", [0.0, 0.9])
+def test_decode_steps_with_every_expert_in_use(dtype, act):
+    """Decode steps over pages against contiguous caches with as many experts per token as there
+    are, so that no near-tie of the router can send a token elsewhere: always compared."""
+    cfg = _cfg(dtype, n_experts=2)
+    W = RI.block_weights(cfg, 11, attn_std=0.08, halt_b=-1.0)
+    blk = R.RecurrentBlock(cfg, to_dev(W))
+    B, T, L, t_max = 3, 24, 3, 32
+    h0, e = (t.cuda() for t in RI.recurrent_inputs(cfg, B, T, 12))
+    k = torch.zeros(L, B, cfg.n_kv_heads, t_max, cfg.head_dim, dtype=blk.dtype, device="cuda")
+    flat = R.KVCache(k, torch.zeros_like(k))
+    paged = _paged(cfg, L, B, t_max, 16, False, 1)
+    for cache in (flat, paged):
+        blk.forward(h0, e, B, T, L, act, cache=cache)
+    start = torch.tensor([T, 4, T - 1], dtype=torch.int32, device="cuda")
+    g = torch.Generator().manual_seed(13)
+    for i in range(3):
+        hd = torch.randn(B, cfg.dim, generator=g).cuda()
+        ed = torch.randn(B, cfg.dim, generator=g).to(blk.dtype).cuda()
+        x = [t.clone() for t in blk.decode_step(hd, ed, start + i, flat, L, act)]
+        y = blk.decode_step(hd, ed, start + i, paged, L, act)
+        assert torch.equal(x[2].sort(-1).values, y[2].sort(-1).values)
+        _close(y[0], x[0], dtype)
+        _close(y[1], x[1], dtype)
+
+
+def test_generation_steps_fed_the_same_tokens():
+    """Each step of generation over pages, given the contiguous run's token, has its logits."""
+    wl = RI.get_workload("tiny_gqa_fp32")
+    MW = to_dev(RI.model_weights(wl.cfg, wl.seed))
+    ids = torch.randint(0, wl.cfg.vocab_size, (2, 16), generator=torch.Generator().manual_seed(31)).int().cuda()
+    flat = R.Generator(wl.cfg, MW, 2, 16, 8, 4)
+    gens = [R.Generator(wl.cfg, MW, 2, 16, 8, 4, page_size=8, cuda_graph=g) for g in (True, False)]
+    for s in range(8):
+        for gen in [flat] + gens:
+            gen.decode(s) if s else gen.prefill(ids)
+        for gen in gens:
+            _close(gen.logits, flat.logits, "fp32")
+            gen.tokens[s].copy_(flat.tokens[s])
+
+
 def test_sampling_changed_between_generations():
     """A generator whose parameters are changed draws with the new ones, replayed or not; values
     changed inside a parameter's tensor count at once."""
