@@ -139,13 +139,15 @@ class PagedKVCache:
     def alloc(cfg, n_loops: int, batch: int, t_max: int, page_size: int = 64, quantised: bool = False,
               n_pages: Optional[int] = None, page_table: Optional[torch.Tensor] = None, device=None) -> "PagedKVCache":
         """Zeroed pages for `batch` sequences of up to t_max positions.  Without a page_table
-        every sequence gets its own pages, one after another; with one (int32 [batch, max_pages])
-        n_pages says how many pages to hold."""
+        every sequence gets its own pages, one after another (n_pages, if given, may hold more); with
+        one (int32 [batch, max_pages]) n_pages says how many pages to hold."""
         if cfg.attn_type != "gqa":
             raise ValueError("a paged cache holds GQA keys and values")
         device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
         if page_table is None:
             per = -(-t_max // page_size)
+            if n_pages is not None and n_pages < batch * per:
+                raise ValueError(f"n_pages: {batch} sequences of {t_max} positions need {batch * per}, got {n_pages}")
             page_table = torch.arange(batch * per, dtype=torch.int32, device=device).reshape(batch, per)
             n_pages = batch * per if n_pages is None else n_pages
         elif n_pages is None:
