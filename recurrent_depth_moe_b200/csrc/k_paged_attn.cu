@@ -4,9 +4,9 @@
 // head), so the floor is the cache's bytes at HBM rate.
 //
 // The work is one line of tiles: (sequence, kv head and group of 8 query heads, keys).  The
-// grid is what the GPU holds at once, and its i-th worker takes the i-th equal piece of the
-// line, so ragged lengths and any batch keep every worker busy to the end; the lengths stay on
-// the device.  A worker walks its piece with the running maximum m and sum l of a softmax
+// grid is what the GPU holds at once (up to 128 channels), and its i-th worker takes the i-th
+// equal piece of the line, so ragged lengths and any batch keep every worker busy to the end; the
+// lengths stay on the device.  A worker walks its piece with the running maximum m and sum l of a softmax
 // (base-2 logarithms).  A (sequence, head group) that one worker walks whole is written at
 // once; where it is spread over several, k_paged_attn_join joins their parts,
 //   o = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s.
@@ -1028,6 +1028,10 @@ bool mma_takes(int dtype, const PagedView& c) {
   const int rb = c.hd * (c.e4m3 ? 1 : 2);
   return dtype == 1 && c.hd % 8 == 0 && rb % 16 == 0 && !(((uintptr_t)c.k | (uintptr_t)c.v) & 15);
 }
+// Above 128 channels an SM holds one CTA, and the same grid runs in two (bf16) or three waves.  A grid
+// of one wave takes, us at 256 channels, 16 heads on 4: 32 sequences of 4097 to 8191 keys in bf16 160
+// (170), in e4m3 150 (166); 64 of 1 to 4224 76 (70), 57 (76); 4 of 37 29 (22), 27 (22): less for long
+// lines, more for short ones.
 int ctas_mma(bool e4m3) { return device_sm_count() * (e4m3 ? Tile<128, true>::CTAS : Tile<128, false>::CTAS); }
 constexpr int SIMT_CTAS = 5;   // on an SM at most (an fp32 tile of 128 channels, twice, is 68 KB: three)
 int ctas_simt(int smem) { return device_sm_count() * std::max(1, std::min(SIMT_CTAS, 227 * 1024 / (smem + 4096))); }
