@@ -260,15 +260,15 @@ template <typename T, bool Q> void write_t(const PagedWriteParams& p, cudaStream
 #undef RDT_W
 }
 template <typename T, bool Q> void read_t(const PagedReadParams& p, cudaStream_t s) {
-  const int n = Vec<T>::N;
+  const int n = Vec<T>::N, most = std::min(p.t_out, p.c.max_pages * p.c.page_size);   // (a table holds 2^30 positions at most)
   note_launch();
   if (p.c.hd % n || !on16(p.c.k, p.c.v) || !on16(p.k_out, p.v_out)) {
-    k_paged_read<T, Q><<<dim3((unsigned)((p.t_out + 3) / 4), (unsigned)p.c.Hkv, (unsigned)p.B), NT, 0, s>>>(p);
+    k_paged_read<T, Q><<<dim3((unsigned)((most + 3) / 4), (unsigned)p.c.Hkv, (unsigned)p.B), NT, 0, s>>>(p);
     return;
   }
   // two rounds of the threads' pieces
   const int rt = std::max(1, std::min(NT, 2 * 4 * NT / (p.c.hd / n)));
-  k_paged_read_vec<T, Q><<<dim3((unsigned)((p.t_out + rt - 1) / rt), (unsigned)p.c.Hkv, (unsigned)p.B), NT, 0, s>>>(p, rt);
+  k_paged_read_vec<T, Q><<<dim3((unsigned)((most + rt - 1) / rt), (unsigned)p.c.Hkv, (unsigned)p.B), NT, 0, s>>>(p, rt);
 }
 }  // namespace
 
