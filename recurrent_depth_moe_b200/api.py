@@ -364,9 +364,9 @@ class DepthBatch:
     block once over all slots, each slot's token at its own loop, and a token that halts
     leaves its slot to the sequence's next token (after its remaining loops' keys / values
     are written from its frozen state).  The caches are contiguous (KVCache).  Results equal
-    n_tokens successive decode_step calls per sequence.  h0 [B, S, D] fp32, e [B, S, D] model dtype, cache_len [B] int32 (position
-    of token 0), halt_logit_offset [B, S] fp32 or None.  Outputs: h_out [B, S, D],
-    halt_weights [B, S, L], expert_ids [B, S, L, k]."""
+    n_tokens successive decode_step calls per sequence.  h0 [B, S, D] fp32, e [B, S, D] model
+    dtype, cache_len [B] int32 (position of token 0), halt_logit_offset [B, S] fp32 or None.
+    Outputs: h_out [B, S, D], halt_weights [B, S, L], expert_ids [B, S, L, k]."""
 
     def __init__(self, blk: "RecurrentBlock", h0: torch.Tensor, e: torch.Tensor, cache_len: torch.Tensor,
                  cache: KVCache, n_loops: int, act_threshold: float = 0.0,

@@ -6,8 +6,8 @@
 // The work is one line of tiles: (sequence, kv head and group of 8 query heads, keys).  The
 // grid is what the GPU holds at once (up to 128 channels), and its i-th worker takes the i-th
 // equal piece of the line, so ragged lengths and any batch keep every worker busy to the end; the
-// lengths stay on the device.  A worker walks its piece with the running maximum m and sum l of a softmax
-// (base-2 logarithms).  A (sequence, head group) that one worker walks whole is written at
+// lengths stay on the device.  A worker walks its piece with the running maximum m and sum l of a
+// softmax (base-2 logarithms).  A (sequence, head group) that one worker walks whole is written at
 // once; where it is spread over several, k_paged_attn_join joins their parts,
 //   o = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s.
 //

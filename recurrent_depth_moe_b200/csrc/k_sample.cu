@@ -24,8 +24,8 @@
 // and histograms over their (logit, index) order narrow the border to at most 32 of them, which
 // one warp ranks.  The kept tokens are then those at or before one (logit, index) pair.
 //
-// Measured on one B200, us: a row of 201,088 logits with top-p 29; 64 such rows with mixed
-// parameters 69; 256 with top-p 312 (the logits at the copy rate: 31).  Each row passes up to seven
+// Measured on one B200, us: a row of 201,088 logits with top-p 30; 64 such rows with mixed
+// parameters 67; 256 with top-p 305 (the logits at the copy rate: 31).  Each row passes up to seven
 // cluster barriers, each about 2 us with the remote reads behind it, and that chain bounds it: of
 // 44 us that a wave of 37 clusters takes, 7 are the load, 15 the passes and 20 the barriers and
 // exchanges.
