@@ -403,7 +403,8 @@ RDT_API rdt_status rdt_paged_attention(const rdt_paged_cache* cache, int loop, c
  * decode step attends with rdt_paged_attention's kernel; a prefill at start_pos 0 attends to
  * its own rows as projected, one at start_pos > 0 to positions 0 .. start_pos + seq - 1 read
  * back from the pages (rows of zeros where a table entry is out of range; the decode step leaves
- * such positions out).  cache_len and the table are read on the device.  ws:
+ * such positions out).  cache_len and the table are read on the device; a cache_len[b] out of
+ * range is recorded, and nothing of sequence b is written.  ws:
  * rdt_paged_workspace_size bytes for the call's batch, seq and start_pos (0 for a decode step),
  * used as any other workspace; its first bytes are the call's status word (of the latest call
  * alone; the cache's own keeps what was recorded until it is read). */

@@ -76,13 +76,12 @@ __device__ __forceinline__ int page_of(const PagedView& c, int b, int pos, DevSt
 // Visible keys of sequence b: its length (0 without lens) plus len_add, inside what its table can hold.
 __device__ __forceinline__ int visible_keys(const PagedView& c, const int* lens, int b, int len_add, DevStatus* st,
                                             int where) {
-  const int n = (lens ? __ldg(lens + b) : 0) + len_add;
-  const long long cap = (long long)c.max_pages * c.page_size;
+  const long long n = (long long)(lens ? __ldg(lens + b) : 0) + len_add, cap = (long long)c.max_pages * c.page_size;
   if (n > cap) {
-    record_bad(c, st, where, n);
+    record_bad(c, st, where, (int)(n - len_add));
     return (int)cap;
   }
-  return n > 0 ? n : 0;
+  return n > 0 ? (int)n : 0;
 }
 
 }  // namespace rdt

@@ -171,6 +171,7 @@ struct Ctx {
   bool test_mla_done = false;      // ... and its attention was launched
   const rdt_paged_cache* paged = nullptr;   // GQA keys / values in pages instead of a rdt_kv_cache
   size_t paged_off = 0;                     // its part of the workspace, behind the layout
+  const int* paged_len = nullptr;           // decode: the lengths as given (pos holds them clamped)
 };
 
 // What a paged cache needs behind the layout: the decode attention's parts, or for a prefill
@@ -287,7 +288,8 @@ rdt_status attention_block(Ctx& x, int B, int T, const float* combined, const vo
         memset(&pw, 0, sizeof(pw));
         pw.c = paged_view(x.paged, loop_t);
         pw.k = (const char*)qkv + (size_t)H * hd * es; pw.v = (const char*)qkv + (size_t)(H + Hkv) * hd * es; pw.ld = W;
-        pw.pos = pos; pw.n_rows = N; pw.seq = T; pw.st = x.st;
+        // (a decode step: a length out of range writes nothing, since other sequences may share the pages)
+        pw.pos = decode ? x.paged_len : pos; pw.n_rows = N; pw.seq = T; pw.st = x.st;
         launch_paged_write(x.dtype, pw, x.s);
       }
       if (decode) {
@@ -295,7 +297,7 @@ rdt_status attention_block(Ctx& x, int B, int T, const float* combined, const vo
         memset(&pa, 0, sizeof(pa));
         pa.c = paged_view(x.paged, loop_t);
         pa.q = qkv; pa.q_row = W; pa.o = attn; pa.o_row = (long long)H * hd;
-        pa.lens = pos; pa.len_add = 1;      // the new token's own position included
+        pa.lens = x.paged_len; pa.len_add = 1;   // the new token's own position included
         pa.B = B; pa.H = H; pa.scale = ap.scale; pa.scratch = at<void*>(x.ws, x.paged_off); pa.st = x.st;
         ProfScope ps(PC_ATTN, x.s);
         RDT_TRY(launch_paged_attn(x.dtype, pa, x.s));
@@ -588,6 +590,7 @@ rdt_status run_recurrent(const rdt_config* c, const rdt_weights* w, const float*
   make_layout(c, B, T, max_keys, &x.L);
   x.paged = paged;
   x.paged_off = x.L.total;
+  x.paged_len = cache_len;
   if ((st = check_ws(ws, ws_bytes, x.L)) != RDT_OK) return st;
   if (paged && ws_bytes < x.L.total + paged_ws_bytes(c, paged, B, T, start_pos, decode)) return RDT_ERR_WORKSPACE;
   // halted rows drop out of the attention queries and the O projection (prefill with ACT,
@@ -938,6 +941,7 @@ static rdt_status block_forward(const rdt_config* cfg, const rdt_weights* w, con
   make_layout(cfg, batch, seq, max_keys, &x.L);
   x.paged = paged;
   x.paged_off = x.L.total;
+  x.paged_len = cache_len;
   if ((st = check_ws(ws, ws_bytes, x.L)) != RDT_OK) return st;
   if (paged && ws_bytes < x.L.total + paged_ws_bytes(cfg, paged, batch, seq, start_pos, decode)) return RDT_ERR_WORKSPACE;
   x.st = at<DevStatus*>(ws, x.L.status);

@@ -222,3 +222,40 @@ def test_greedy_generation_reads_no_uniform_numbers():
     gen = R.Generator(wl.cfg, MW, 2, 16, 4, 4)
     gen.u = gen.u_in = None
     assert torch.equal(gen.run(ids), want)
+
+
+@pytest.mark.parametrize("quantised", [False, True])
+def test_a_length_out_of_range_writes_nothing(quantised):
+    """A decode step whose sequence has no valid position, over pages that others read (a common
+    prefix): recorded, and the pages hold what they held but for the other sequence's new row,
+    whose output is what it is alone."""
+    cfg = _cfg("bf16")
+    B, cap = 2, 48
+    blk = R.Block(cfg, to_dev(RI.dense_block_weights(cfg, 5)))
+    rec = R.RecurrentBlock(cfg, to_dev(RI.block_weights(cfg, 21, attn_std=0.08)))
+    x = torch.randn(B * 20, cfg.dim, generator=torch.Generator().manual_seed(6)).cuda()
+    row = x[:B].contiguous()
+    clen = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    for loops, prefill, step in (
+            (1, lambda c: blk.forward(x, B, 20, 0, cache=c), lambda c, n: blk.forward(row, B, 1, 0, cache=c, cache_len=n)),
+            (2, lambda c: rec.forward(x, x.to(torch.bfloat16), B, 20, 2, cache=c),
+             lambda c, n: rec.decode_step(row, row.to(torch.bfloat16), n, c, 2)[0].clone())):
+        cache = _paged(cfg, loops, B, cap, 16, quantised)
+        prefill(cache)
+        cache.page_table[1] = cache.page_table[0]
+        bits = [t.view(torch.uint8) for t in (cache.k, cache.v)] + ([cache.k_exp, cache.v_exp] if quantised else [])
+        held = [t.clone() for t in bits]
+        want = step(cache, clen(20, 21))[0].clone()                   # (position 21 is past what sequence 0 sees)
+        after = [t.clone() for t in bits]
+        page, slot = int(cache.page_table[0, 1]), 4
+        assert cache.read_status() == 0
+        for bad in (-1, cap, cap + 16, 1 << 30, 2 ** 31 - 1, -2 ** 31):
+            for t, h in zip(bits, held):
+                t.copy_(h)
+            got = step(cache, clen(20, bad))
+            assert cache.read_status() == BOUNDS, bad
+            assert torch.equal(got[0], want), bad
+            for t, h, a in zip(bits, held, after):
+                h = h.clone()
+                h[:, page, :, slot] = a[:, page, :, slot]
+                assert torch.equal(t, h), bad
